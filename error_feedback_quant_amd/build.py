@@ -9,6 +9,8 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -17,7 +19,7 @@ LIB = os.path.join(PKG, "libecho.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 HIP_FLAGS = [
-    "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared",
+    "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
     "-ffp-contract=off", "-fno-gpu-flush-denormals-to-zero",
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-Wall", "-Wno-unused-command-line-argument",
@@ -25,7 +27,7 @@ HIP_FLAGS = [
 
 
 def sources():
-    return [os.path.join(CSRC, "echo_api.hip")]
+    return [os.path.join(CSRC, "echo_api.hip"), os.path.join(CSRC, "echo_block_api.hip")]
 
 
 # test-only device code: the kernels' helpers evaluated on their own, built
@@ -34,36 +36,37 @@ CHECK_SRC = os.path.join(ROOT, "tests", "c", "recip_scale_check.hip")
 CHECK_LIB = os.path.join(ROOT, "tests", "c", "librecip_scale_check.so")
 
 
-def build(verbose: bool = False) -> str:
-    tmp = LIB + ".tmp"
-    cmd = [HIPCC, *HIP_FLAGS, "-I", os.path.join(ROOT, "include"), "-I", CSRC, *sources(), "-o", tmp]
+def _hipcc(args, what: str, verbose: bool) -> None:
+    cmd = [HIPCC, *HIP_FLAGS, *args]
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, capture_output=True, text=True)
     # the host pass does not know the packed-fp32 target feature and says so; drop that line
-    noise = "is not a recognized feature for this target"
-    msgs = [l for l in (r.stderr or "").splitlines() if noise not in l]
+    msgs = [l for l in (r.stderr or "").splitlines() if "is not a recognized feature for this target" not in l]
     if r.returncode != 0:
         sys.stderr.write("\n".join(msgs) + "\n")
-        raise RuntimeError(f"hipcc failed ({r.returncode}) building {LIB}")
+        raise RuntimeError(f"hipcc failed ({r.returncode}) building {what}")
     if msgs and verbose:
         sys.stderr.write("\n".join(msgs) + "\n")
-    os.replace(tmp, LIB)
-    build_check(verbose)
+
+
+def build(verbose: bool = False) -> str:
+    with tempfile.TemporaryDirectory() as tmp:
+        objs = [os.path.join(tmp, os.path.basename(s) + ".o") for s in sources()]
+        inc = ["-I", os.path.join(ROOT, "include"), "-I", CSRC]
+        with ThreadPoolExecutor(max_workers=len(objs) + 1) as pool:
+            jobs = [pool.submit(_hipcc, [*inc, "-c", s, "-o", o], s, verbose) for s, o in zip(sources(), objs)]
+            jobs.append(pool.submit(build_check, verbose))
+            for j in jobs:
+                j.result()
+        _hipcc(["-shared", *objs, "-o", LIB + ".tmp"], LIB, verbose)
+    os.replace(LIB + ".tmp", LIB)
     return LIB
 
 
 def build_check(verbose: bool = False) -> str:
-    tmp = CHECK_LIB + ".tmp"
-    cmd = [HIPCC, *HIP_FLAGS, "-I", CSRC, CHECK_SRC, "-o", tmp]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    msgs = [l for l in (r.stderr or "").splitlines() if "is not a recognized feature for this target" not in l]
-    if r.returncode != 0:
-        sys.stderr.write("\n".join(msgs) + "\n")
-        raise RuntimeError(f"hipcc failed ({r.returncode}) building {CHECK_LIB}")
-    os.replace(tmp, CHECK_LIB)
+    _hipcc(["-shared", "-I", os.path.join(ROOT, "include"), "-I", CSRC, CHECK_SRC, "-o", CHECK_LIB + ".tmp"], CHECK_LIB, verbose)
+    os.replace(CHECK_LIB + ".tmp", CHECK_LIB)
     return CHECK_LIB
 
 

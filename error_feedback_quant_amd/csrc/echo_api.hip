@@ -19,11 +19,14 @@
 
 #include "echo.h"
 #include "echo_gemm.hpp"
+#include "echo_host.hpp"
 #include "echo_kernels.hpp"
 
 namespace {
 
-thread_local int t_last_hip_error = 0;
+using echo::aligned16;
+using echo::check_launch;
+using echo::hip_fail;
 
 constexpr int64_t kMaxN = int64_t(1) << 34;
 // passes of 16 groups per block (each DPP row handles this many groups),
@@ -39,20 +42,6 @@ constexpr int64_t kMaxTiles = 4096;
 constexpr int64_t kBatchBelowBlocks = 4096;
 // one-tile calls of at most this many elements per rank run as one launch (onepass_kernel)
 constexpr int64_t kOnePassMaxElems = int64_t(1) << 20;
-
-int hip_fail(hipError_t e)
-{
-    t_last_hip_error = (int)e;
-    return ECHO_EHIP;
-}
-
-int check_launch()
-{
-    hipError_t e = hipGetLastError();
-    return e == hipSuccess ? ECHO_OK : hip_fail(e);
-}
-
-bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
 int64_t code_bytes(int64_t n, int bits) { return bits == 4 ? n / 2 : n; }
 
@@ -373,16 +362,16 @@ const char* echo_status_str(int status)
     switch (status) {
     case ECHO_OK: return "ok";
     case ECHO_EINVAL: return "invalid argument";
-    case ECHO_EALIGN: return "pointer not 16-byte aligned";
-    case ECHO_EUNSUP: return "unsupported bits, group or output dtype";
-    case ECHO_ESHAPE: return "invalid message or tile shape";
+    case ECHO_EALIGN: return "pointer not aligned (16 bytes; block operators: its element)";
+    case ECHO_EUNSUP: return "unsupported bits, group or dtype";
+    case ECHO_ESHAPE: return "invalid message, tile or matrix shape";
     case ECHO_EHIP: return "HIP runtime error";
     case ECHO_ETOOBIG: return "message needs more workspace than the static scratch of the allocation-free call";
     default: return "unknown status";
     }
 }
 
-int echo_last_hip_error(void) { return t_last_hip_error; }
+int echo_last_hip_error(void) { return echo::t_last_hip_error; }
 
 int echo_quantize_ef(const uint16_t* x_bf16, const float* comp, int64_t n, int P, int rank,
                      int64_t tile_begin, int64_t tile_len, int bits, int group, uint8_t* codes,

@@ -29,6 +29,7 @@ _lib = ctypes.CDLL(LIB_PATH)
 
 OK, EINVAL, EALIGN, EUNSUP, ESHAPE, EHIP, ETOOBIG = 0, -1, -2, -3, -4, -5, -6
 OUT_F32, OUT_BF16 = 0, 1
+F32, BF16, I8 = 0, 1, 2
 ERR_NEGATED = 1
 QUANT_NAIVE, QUANT_SYMMETRIC = 2, 4
 X_ALL = 8
@@ -54,6 +55,30 @@ class SimArgs(Structure):
         ("n", c_int64),
         ("x", c_void_p * MAX_P), ("comp", c_void_p * MAX_P), ("slow", c_void_p * MAX_P),
         ("err", c_void_p * MAX_P), ("out", c_void_p * MAX_P),
+        ("workspace", c_void_p), ("workspace_bytes", c_size_t),
+    ]
+
+
+class NormArgs(Structure):
+    """Mirror of echo_norm_args."""
+    _fields_ = [
+        ("T", c_int64), ("H", c_int64),
+        ("ld_x", c_int64), ("ld_r", c_int64), ("ld_r_out", c_int64), ("ld_h", c_int64), ("ld_gate", c_int64),
+        ("gate_tokens", c_int64),
+        ("x_dtype", c_int), ("r_dtype", c_int), ("w_dtype", c_int), ("h_dtype", c_int), ("post", c_int),
+        ("eps", c_float), ("res_scale", c_float), ("block_scale", c_float),
+        ("x", c_void_p), ("r", c_void_p), ("w_post", c_void_p), ("w_pre", c_void_p), ("gate", c_void_p),
+        ("r_out", c_void_p), ("h", c_void_p), ("h_scale", c_void_p),
+    ]
+
+
+class NormGrads(Structure):
+    """Mirror of echo_norm_grads."""
+    _fields_ = [
+        ("ld_dh", c_int64), ("ld_dr_out", c_int64), ("ld_dx", c_int64), ("ld_dr", c_int64), ("ld_dgate", c_int64),
+        ("dh_dtype", c_int),
+        ("dh", c_void_p), ("dr_out", c_void_p), ("dx", c_void_p), ("dr", c_void_p),
+        ("dw_post", c_void_p), ("dw_pre", c_void_p), ("dgate", c_void_p),
         ("workspace", c_void_p), ("workspace_bytes", c_size_t),
     ]
 
@@ -84,6 +109,22 @@ _lib.echo_allreduce_sim_noalloc.restype = c_int
 _lib.echo_allreduce_sim_noalloc.argtypes = [POINTER(SimArgs), c_void_p]
 _lib.echo_noalloc_scratch_bytes.restype = c_size_t
 _lib.echo_noalloc_scratch_bytes.argtypes = []
+_lib.echo_quantize_tokens.restype = c_int
+_lib.echo_quantize_tokens.argtypes = [c_void_p, c_int64, c_int, c_int64, c_int64, c_void_p, c_int64, c_void_p, c_void_p]
+_lib.echo_gemm_int8.restype = c_int
+_lib.echo_gemm_int8.argtypes = [c_void_p, c_int64, c_void_p, c_void_p, c_int64, c_void_p, c_void_p, c_int64, c_int64,
+                                c_int64, c_void_p, c_int64, c_int, c_void_p]
+_lib.echo_linear_int8_workspace_bytes.restype = c_size_t
+_lib.echo_linear_int8_workspace_bytes.argtypes = [c_int64, c_int64, c_int64]
+_lib.echo_linear_int8.restype = c_int
+_lib.echo_linear_int8.argtypes = [c_void_p, c_int64, c_int, c_void_p, c_int64, c_void_p, c_void_p, c_int64, c_int64,
+                                  c_int64, c_void_p, c_int64, c_int, c_void_p, c_size_t, c_void_p]
+_lib.echo_block_norm.restype = c_int
+_lib.echo_block_norm.argtypes = [POINTER(NormArgs), c_void_p]
+_lib.echo_block_norm_backward_workspace_bytes.restype = c_size_t
+_lib.echo_block_norm_backward_workspace_bytes.argtypes = [c_int64, c_int64]
+_lib.echo_block_norm_backward.restype = c_int
+_lib.echo_block_norm_backward.argtypes = [POINTER(NormArgs), POINTER(NormGrads), c_void_p]
 
 
 def lib():
@@ -197,3 +238,140 @@ def echo_allreduce_sim_noalloc(args: SimArgs, stream=None):
 
 def echo_noalloc_scratch_bytes() -> int:
     return int(_lib.echo_noalloc_scratch_bytes())
+
+
+# ---------------------------------------------------------- block operators --
+
+_DTYPES = {torch.float32: F32, torch.bfloat16: BF16, torch.int8: I8}
+
+
+def echo_quantize_tokens(x, ldx, x_dtype, T, K, codes, ldq, scales, stream=None):
+    _check("echo_quantize_tokens", _lib.echo_quantize_tokens(
+        _ptr(x), ldx, x_dtype, T, K, _ptr(codes), ldq, _ptr(scales), _stream(stream)))
+
+
+def echo_gemm_int8(x, ldx, sx, w, ldw, sw, bias, M, N, K, y, ldy, y_dtype, stream=None):
+    _check("echo_gemm_int8", _lib.echo_gemm_int8(
+        _ptr(x), ldx, _ptr(sx), _ptr(w), ldw, _ptr(sw), _ptr(bias), M, N, K, _ptr(y), ldy, y_dtype, _stream(stream)))
+
+
+def echo_linear_int8_workspace_bytes(M, N, K) -> int:
+    return int(_lib.echo_linear_int8_workspace_bytes(M, N, K))
+
+
+def echo_linear_int8(x, ldx, x_dtype, w, ldw, sw, bias, M, N, K, y, ldy, y_dtype, workspace, workspace_bytes=None,
+                     stream=None):
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _check("echo_linear_int8", _lib.echo_linear_int8(
+        _ptr(x), ldx, x_dtype, _ptr(w), ldw, _ptr(sw), _ptr(bias), M, N, K, _ptr(y), ldy, y_dtype, _ptr(workspace),
+        workspace_bytes, _stream(stream)))
+
+
+def _rows(t, shape, what, dtypes):
+    """(pointer, row distance) of a matrix of contiguous rows; the C side cannot see a tensor's shape."""
+    if t.shape != shape or t.dtype not in dtypes or (shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{what}: {tuple(t.shape)} {t.dtype} strides {t.stride()}, expected {tuple(shape)} in rows "
+                         f"of contiguous elements of {' or '.join(str(d) for d in dtypes)}")
+    return t.data_ptr(), t.stride(0)
+
+
+def _vector(t, n, what, dtype):
+    if t.shape != (n,) or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{what}: {tuple(t.shape)} {t.dtype}, expected {n} contiguous elements of {dtype}")
+    return t.data_ptr()
+
+
+_FLOATS = (torch.float32, torch.bfloat16)
+_FLOAT = (torch.float32,)
+_ANY_H = (torch.float32, torch.bfloat16, torch.int8)
+
+
+def make_norm_args(x, r=None, r_out=None, h=None, h_scale=None, post=True, w_post=None, w_pre=None, gate=None,
+                   gate_tokens=0, res_scale=1.0, block_scale=1.0, eps=1e-5):
+    """Fill an echo_norm_args from tensors: x, r, r_out and h are [T, H] in
+    contiguous rows, w_post and w_pre [H], gate [ceil(T / gate_tokens), H]."""
+    shape = x.shape
+    T, H = shape
+    a = NormArgs()
+    a.T, a.H = T, H
+    a.post, a.eps, a.res_scale, a.block_scale = 1 if post else 0, eps, res_scale, block_scale
+    a.x, a.ld_x = _rows(x, shape, "x", _FLOATS)
+    a.x_dtype = _DTYPES[x.dtype]
+    rd = r.dtype if r is not None else r_out.dtype if r_out is not None else x.dtype
+    a.r_dtype = _DTYPES.get(rd, -1)
+    if r is not None:
+        a.r, a.ld_r = _rows(r, shape, "r", _FLOATS)
+    if r_out is not None:
+        a.r_out, a.ld_r_out = _rows(r_out, shape, "r_out", (rd,))
+    if h is not None:
+        a.h, a.ld_h = _rows(h[:, :H] if h.dtype == torch.int8 else h, shape, "h", _ANY_H)
+        a.h_dtype = _DTYPES[h.dtype]
+        if h.dtype == torch.int8 and h_scale is not None:
+            a.h_scale = _vector(h_scale, T, "h_scale", torch.float32)
+    wd = next((w.dtype for w in (w_post, w_pre, gate) if w is not None), torch.float32)
+    a.w_dtype = _DTYPES.get(wd, -1)
+    if w_post is not None:
+        a.w_post = _vector(w_post, H, "w_post", wd)
+    if w_pre is not None:
+        a.w_pre = _vector(w_pre, H, "w_pre", wd)
+    if gate is not None:
+        if gate_tokens < 1:
+            raise ValueError("a gate needs gate_tokens >= 1")
+        a.gate_tokens = gate_tokens
+        a.gate, a.ld_gate = _rows(gate, (-(-T // gate_tokens), H), "gate", (wd,))
+    return a
+
+
+def make_norm_grads(dh=None, dr_out=None, dx=None, dr=None, dw_post=None, dw_pre=None, dgate=None, workspace=None,
+                    workspace_bytes=None):
+    """Fill an echo_norm_grads from tensors, shaped as in make_norm_args.
+    Whether they fit its arguments (shape, types of dx, dr and dr_out, rows of
+    dgate) is checked by echo_block_norm_backward."""
+    g = NormGrads()
+    g.shape = next((t.shape for t in (dh, dr_out, dx, dr) if t is not None), None)
+    g.types = set()
+    if dh is not None:
+        g.dh, g.ld_dh = _rows(dh, g.shape, "dh", _FLOATS)
+        g.dh_dtype = _DTYPES[dh.dtype]
+    if dr_out is not None:
+        g.dr_out, g.ld_dr_out = _rows(dr_out, g.shape, "dr_out", _FLOATS)
+        g.types.add(("r", _DTYPES[dr_out.dtype]))
+    if dr is not None:
+        g.dr, g.ld_dr = _rows(dr, g.shape, "dr", _FLOATS)
+        g.types.add(("r", _DTYPES[dr.dtype]))
+    if dx is not None:
+        g.dx, g.ld_dx = _rows(dx, g.shape, "dx", _FLOATS)
+        g.types.add(("x", _DTYPES[dx.dtype]))
+    H = g.shape[1] if g.shape is not None else 0
+    if dw_post is not None:
+        g.dw_post = _vector(dw_post, H, "dw_post", torch.float32)
+    if dw_pre is not None:
+        g.dw_pre = _vector(dw_pre, H, "dw_pre", torch.float32)
+    g.gate_rows = None
+    if dgate is not None:
+        g.gate_rows = dgate.shape[0]
+        g.dgate, g.ld_dgate = _rows(dgate, (g.gate_rows, H), "dgate", _FLOAT)
+    g.workspace = _ptr(workspace)
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    g.workspace_bytes = workspace_bytes
+    return g
+
+
+def echo_block_norm(args: NormArgs, stream=None):
+    _check("echo_block_norm", _lib.echo_block_norm(ctypes.byref(args), _stream(stream)))
+
+
+def echo_block_norm_backward_workspace_bytes(T, H) -> int:
+    return int(_lib.echo_block_norm_backward_workspace_bytes(T, H))
+
+
+def echo_block_norm_backward(args: NormArgs, grads: NormGrads, stream=None):
+    if getattr(grads, "shape", None) is not None:
+        kinds = {"x": args.x_dtype, "r": args.r_dtype}
+        if (grads.shape != (args.T, args.H) or any(kinds[k] != d for k, d in grads.types)
+                or grads.gate_rows not in (None, -(-args.T // args.gate_tokens) if args.gate else 0)):
+            raise ValueError("the gradients' shapes or types do not fit the forward call's arguments")
+    _check("echo_block_norm_backward", _lib.echo_block_norm_backward(
+        ctypes.byref(args), ctypes.byref(grads), _stream(stream)))

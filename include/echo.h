@@ -30,7 +30,9 @@
  *    they do not synchronize.
  *  - Arguments are checked on the host before anything is enqueued; a call
  *    that returns an error other than ECHO_EHIP has enqueued nothing.
- *  - Data pointers must be 16-byte aligned (ECHO_EALIGN otherwise).
+ *  - Data pointers must be 16-byte aligned (ECHO_EALIGN otherwise); the block
+ *    operators at the end have conventions of their own for this and for
+ *    non-finite inputs.
  *  - Messages: n elements per rank, 0 <= n <= 2^34, n a multiple of P*group.
  *    S = n / P is the segment length.  Tiles are element ranges *inside each
  *    segment*: [tile_begin, tile_begin + tile_len), both multiples of group,
@@ -62,8 +64,8 @@ extern "C" {
 enum echo_status {
     ECHO_OK = 0,
     ECHO_EINVAL = -1, /* null required pointer, bad P/rank/owner/constants */
-    ECHO_EALIGN = -2, /* a data pointer is not 16-byte aligned */
-    ECHO_EUNSUP = -3, /* bits not 4/8, group not 128/256, unknown output dtype */
+    ECHO_EALIGN = -2, /* a data pointer is not 16-byte aligned (block operators: not aligned to its element) */
+    ECHO_EUNSUP = -3, /* bits not 4/8, group not 128/256, unknown dtype */
     ECHO_ESHAPE = -4, /* n or tile not a valid multiple / out of range */
     ECHO_EHIP = -5,   /* a HIP launch or runtime call failed; see echo_last_hip_error */
     ECHO_ETOOBIG = -6 /* echo_allreduce_sim_noalloc: the message needs more workspace than
@@ -71,6 +73,9 @@ enum echo_status {
 };
 
 enum echo_out_dtype { ECHO_OUT_F32 = 0, ECHO_OUT_BF16 = 1 };
+
+/* element types of the block operators (same values as echo_out_dtype) */
+enum echo_dtype { ECHO_F32 = 0, ECHO_BF16 = 1, ECHO_I8 = 2 };
 
 /* flags for echo_quantize_ef / echo_reduce_segment / echo_gemm_quantize_ef
  * (and echo_sim_args.quant for the two quantizer bits) */
@@ -344,6 +349,150 @@ int echo_allreduce_sim_noalloc(const echo_sim_args* args, void* stream);
 
 /* Size in bytes of the static scratch array of echo_allreduce_sim_noalloc. */
 size_t echo_noalloc_scratch_bytes(void);
+
+/*
+ * The block operators: what stands on both sides of the all-reduce in a
+ * tensor-parallel block.  A row-parallel layer in 8-bit integers makes the
+ * partial sums; the norms that close the block and open the next one take
+ * the summed output.
+ *
+ * Conventions, beside those above:
+ *  - A matrix is rows of contiguous elements at a distance of ld elements
+ *    (ld >= the row's length; a single row's ld is not used).  Nothing
+ *    outside the rows is read or written.
+ *  - Pointers need the alignment of their element type only (workspaces 16
+ *    bytes); where the base and ld of every matrix of a call are multiples of
+ *    16 bytes the call is fastest.
+ *  - Non-finite values: an infinity or a NaN in a token makes results of that
+ *    token non-finite and touches no other token (the sums over tokens in a
+ *    backward pass take it up).
+ *  - Inputs and outputs do not overlap except where a call says so.
+ */
+
+/*
+ * echo_quantize_tokens — 8-bit codes and one scale for each token.
+ *   a = max(max_k |x[t][k]|, 2^-100),  scales[t] = a / 127,
+ *   codes[t][k] = rint(x[t][k] * (127 / a)), in [-127, 127]
+ * in single IEEE fp32 operations, rint half to even.  A token with an
+ * infinity or a NaN gets the scale NaN and codes 0.
+ *
+ *   x (device, in)       [T][K], ECHO_F32 or ECHO_BF16, rows at ldx
+ *   codes (device, out)  [T][K] rows at ldq
+ *   scales (device, out) [T]
+ * Constraints: 0 <= K <= 131071, 0 <= T < 2^31 (ECHO_ESHAPE).
+ */
+int echo_quantize_tokens(const void* x, int64_t ldx, int x_dtype, int64_t T, int64_t K,
+                         int8_t* codes, int64_t ldq, float* scales, void* stream);
+
+/*
+ * echo_gemm_int8 — product of 8-bit integers with a scale for each token and
+ * each channel:
+ *   y[m][n] = float(sum_k x[m][k] * w[n][k]) * sx[m] * sw[n] (+ bias[n])
+ * The sum is exact (32-bit integers), so results depend on no order; it is
+ * rounded to fp32, multiplied by sx and then by sw, and the bias is added,
+ * each a single fp32 operation; a bf16 y is rounded once more.
+ * With the codes of echo_quantize_tokens and a weight quantized by rows of
+ * its [N][K] form this is the linear layer y = x w^T + bias; its partial sums
+ * (ECHO_BF16, ldy = N) are the message of echo_quantize_ef and
+ * echo_allreduce_sim.
+ *
+ *   x (device, in)   [M][K] codes, rows at ldx; any value of int8
+ *   w (device, in)   [N][K] codes, rows at ldw
+ *   sx, sw (device, in) [M], [N];  bias (device, in) fp32 [N] or NULL
+ *   y (device, out)  [M][N], ECHO_F32 or ECHO_BF16, rows at ldy
+ * Constraints: 0 <= K <= 131071 (the sum stays in 32 bits), M, N < 2^31,
+ * and at most 2^31 - 1 tiles of 64 x 64 (ECHO_ESHAPE).  M or N of 0 enqueues
+ * nothing; K of 0 gives y = bias (or 0).
+ */
+int echo_gemm_int8(const int8_t* x, int64_t ldx, const float* sx, const int8_t* w, int64_t ldw,
+                   const float* sw, const float* bias, int64_t M, int64_t N, int64_t K, void* y,
+                   int64_t ldy, int y_dtype, void* stream);
+
+/*
+ * echo_linear_int8 — echo_quantize_tokens of x followed by echo_gemm_int8, bit
+ * for bit.  The workspace (device, 16-byte aligned, at least
+ * echo_linear_int8_workspace_bytes) holds the codes and scales between the
+ * two; it may be NULL where that function returns 0.
+ */
+size_t echo_linear_int8_workspace_bytes(int64_t M, int64_t N, int64_t K);
+int echo_linear_int8(const void* x, int64_t ldx, int x_dtype, const int8_t* w, int64_t ldw,
+                     const float* sw, const float* bias, int64_t M, int64_t N, int64_t K, void* y,
+                     int64_t ldy, int y_dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * echo_block_norm — the norms that close one block and open the next, around
+ * the gated, scaled residual sum.  For every token:
+ *   z  = x * rsqrt(mean(x^2) + eps) * w_post   (post = 1; z = x for post = 0)
+ *   r' = res_scale * r + block_scale * gate * z
+ *   h  = r' * rsqrt(mean(r'^2) + eps) * w_pre
+ * in fp32; r_out receives r', h the normed stream (rounded once, from the
+ * unrounded r'), as fp32, bf16 or 8-bit codes with a scale for each token
+ * (those of echo_quantize_tokens applied to the unrounded h).
+ *
+ * x is the block's output (the all-reduced sum), r the residual stream.  One
+ * row of the gate serves gate_tokens consecutive tokens: 1 is a gate for each
+ * token, the sequence length one for each sequence, T or more one for all;
+ * the last row may serve fewer.  r NULL is a stream of zeros (the first
+ * norm of a model: post = 0, x the embeddings), w_post, w_pre and gate NULL
+ * are ones, r_out or h may be NULL (not both).  r_out may be r.
+ * Constraints: T < 2^31, H <= 2^30 (ECHO_ESHAPE); eps > 0 and the scales
+ * finite, w_post NULL where post = 0 (ECHO_EINVAL).
+ */
+typedef struct echo_norm_args {
+    int64_t T, H;                                  /* tokens, width */
+    int64_t ld_x, ld_r, ld_r_out, ld_h, ld_gate;   /* row distances in elements */
+    int64_t gate_tokens;                           /* tokens of one gate row, >= 1 with a gate */
+    int x_dtype, r_dtype, w_dtype;                 /* ECHO_F32 or ECHO_BF16; r_dtype also of r_out, w_dtype
+                                                      of w_post, w_pre and gate */
+    int h_dtype;                                   /* ECHO_F32, ECHO_BF16 or ECHO_I8 */
+    int post;                                      /* 1: post norm, 0: none */
+    float eps, res_scale, block_scale;
+    const void* x;                                 /* (device) [T][H] */
+    const void* r;                                 /* (device) [T][H] or NULL */
+    const void* w_post;                            /* (device) [H] or NULL */
+    const void* w_pre;                             /* (device) [H] or NULL */
+    const void* gate;                              /* (device) [ceil(T / gate_tokens)][H] or NULL */
+    void* r_out;                                   /* (device) [T][H] or NULL */
+    void* h;                                       /* (device) [T][H] or NULL */
+    float* h_scale;                                /* (device) [T], required for an ECHO_I8 h */
+} echo_norm_args;
+
+int echo_block_norm(const echo_norm_args* args, void* stream);
+
+/*
+ * echo_block_norm_backward — gradients of echo_block_norm.  args are the
+ * forward call's (its r_out, h and h_scale are not used; r and x have to hold
+ * what they held then, so keep r where the forward call wrote r_out over it).
+ * The gradient of an 8-bit h is taken as that of the unquantized h.
+ *
+ *   dh (device, in)      [T][H] gradient of h, ECHO_F32 or ECHO_BF16, or NULL (zero)
+ *   dr_out (device, in)  [T][H] gradient of r_out in r's type, or NULL (zero)
+ *   dx, dr (device, out) [T][H] in x's and r's type, or NULL; dr may be dr_out
+ *   dw_post, dw_pre (device, out) fp32 [H] or NULL: sums over all tokens
+ *   dgate (device, out)  fp32 [ceil(T / gate_tokens)][H] or NULL: sums over
+ *                        each gate row's tokens
+ * The sums run in fp32 in a fixed order (equal inputs give equal bits).
+ * The workspace (device, 16-byte aligned) has at least
+ * echo_block_norm_backward_workspace_bytes bytes.  T of 0 writes zeros to
+ * dw_post and dw_pre.  ECHO_EINVAL: both dh and dr_out NULL (T > 0), dgate
+ * without a gate, dw_post without the post norm, dr without r.
+ */
+typedef struct echo_norm_grads {
+    int64_t ld_dh, ld_dr_out, ld_dx, ld_dr, ld_dgate;
+    int dh_dtype;
+    const void* dh;
+    const void* dr_out;
+    void* dx;
+    void* dr;
+    float* dw_post;
+    float* dw_pre;
+    float* dgate;
+    void* workspace;
+    size_t workspace_bytes;
+} echo_norm_grads;
+
+size_t echo_block_norm_backward_workspace_bytes(int64_t T, int64_t H);
+int echo_block_norm_backward(const echo_norm_args* args, const echo_norm_grads* grads, void* stream);
 
 /* Static description of a status code. */
 const char* echo_status_str(int status);

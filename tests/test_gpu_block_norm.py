@@ -1,0 +1,338 @@
+"""echo_block_norm and echo_block_norm_backward on the GPU against the plain
+64-bit forms, within the fp32 error bounds derived in _block_ref.py."""
+import itertools
+
+import numpy as np
+import pytest
+import torch
+
+import _block_ref as ref
+from _helpers import DEV, say
+from test_gpu_block_int8 import matrix, same_bits, untouched
+
+pytestmark = pytest.mark.gpu
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+EPS = 1e-5
+
+
+@pytest.fixture(scope="module")
+def echo():
+    from error_feedback_quant_amd import echo as e
+    assert torch.cuda.is_available()
+    return e
+
+
+class Case:
+    """Inputs of one forward call on the GPU (rows at H + pad, `off` elements into their allocations) and in float64."""
+
+    def __init__(self, T, H, x="bf16", r="bf16", w="f32", h="bf16", post=True, gate=0, rho=1.0, beta=1.0, pad=0, off=0,
+                 has_r=True, weights=True, seed=0, scale=1.0):
+        rng = np.random.default_rng(seed + 31 * T + H)
+        t = lambda *s: torch.from_numpy(rng.standard_normal(s).astype(np.float32))  # noqa: E731
+        m = lambda v, dt: matrix(*v.shape, v.shape[1] + pad, DT[dt], v, off)[1]  # noqa: E731
+        vec = lambda v, dt: matrix(1, v.numel(), v.numel(), DT[dt], v[None], off)[1][0]  # noqa: E731
+        self.T, self.H, self.kx, self.kr, self.kh, self.pad, self.off = T, H, x, r, h, pad, off
+        self.post, self.rho, self.beta, self.gate_tokens = post, rho, beta, gate
+        self.x = m(0.7 * t(T, H) * scale, x)
+        self.r = m(1.5 * t(T, H) * scale, r) if has_r else None
+        self.w_post = vec(1 + 0.2 * t(H), w) if post and weights else None
+        self.w_pre = vec(1 + 0.2 * t(H), w) if weights else None
+        self.gate = m(0.5 + 0.3 * t(-(-T // gate), H), w) if gate else None
+        self.up = m(t(T, H), r)
+        self.dh = m(t(T, H), h if h != "i8" else "bf16")
+
+    def out(self, kind):
+        return matrix(self.T, self.H, self.H + self.pad, DT.get(kind, torch.int8), None, self.off)
+
+    def args(self, echo, **kw):
+        return echo.make_norm_args(self.x, self.r, post=self.post, w_post=self.w_post, w_pre=self.w_pre, gate=self.gate,
+                                   gate_tokens=self.gate_tokens, res_scale=self.rho, block_scale=self.beta, eps=EPS, **kw)
+
+    def plain(self):
+        f = ref.f64
+        eps, rho, beta = (float(np.float32(v)) for v in (EPS, self.rho, self.beta))
+        self.rho64, self.beta64 = rho, beta
+        return ref.norm_forward(f(self.x), f(self.r), f(self.w_post), f(self.w_pre), f(self.gate), self.gate_tokens or 1,
+                                self.post, rho, beta, eps)
+
+
+def within(got, want, tol, what):
+    tol = np.broadcast_to(tol, want.shape)
+    bad = ref.outside(got, want, tol)
+    assert not bad.any(), (f"{what}: {int(bad.sum())} of {bad.size} outside; worst {np.abs(ref.f64(got) - want)[bad].max():.3g} "
+                           f"against {tol[bad].max():.3g} before rounding")
+
+
+def check_forward(echo, c):
+    f = c.plain()
+    tr, th = ref.norm_bounds(f)
+    rb, r_out = c.out(c.kr)
+    hb, h = c.out(c.kh)
+    s = torch.full((c.T,), 7.0, device=DEV)
+    echo.echo_block_norm(c.args(echo, r_out=r_out, h=h, h_scale=s if c.kh == "i8" else None))
+    torch.cuda.synchronize()
+    within(r_out, f["rn"], tr, "r_out")
+    if c.kh == "i8":
+        # the scale is the largest |h| over 127 (one division, the error of
+        # h), a code is off its value by half a step and h's error, and the
+        # decode here runs in float64
+        amax, worst = np.abs(f["h"]).max(1), th.max(1)
+        s64 = ref.f64(s)
+        assert (np.abs(s64 * 127 - amax) <= 1.01 * worst + 4 * ref.U * amax + 2.0 ** -99).all()
+        far = np.abs(ref.f64(h) - f["h"] / s64[:, None])
+        assert (far <= 0.5 + th / s64[:, None] + 4 * ref.U * 128).all(), far.max()
+        assert int(h.abs().max()) <= 127
+    else:
+        within(h, f["h"], th, "h")
+    untouched(rb, r_out)
+    untouched(hb, h)
+    return r_out, h, s
+
+
+SIZES = [(1, 1), (1, 4096), (3, 7), (2, 64), (64, 1024), (65, 100), (7, 1000), (333, 1537), (5, 2048), (40, 4096), (9, 5120),
+         (6, 8192), (3, 8193), (4, 16384), (3, 16392), (2, 20000)]
+
+
+@pytest.mark.parametrize("T,H", SIZES)
+@pytest.mark.parametrize("x,r,h", list(itertools.product(["bf16", "f32"], ["bf16", "f32"], ["bf16", "f32", "i8"])))
+def test_forward_sizes_and_types(echo, T, H, x, r, h):
+    say("norm", T, H, x, r, h)
+    check_forward(echo, Case(T, H, x, r, "f32" if T % 2 else "bf16", h, gate=max(1, T // 2), rho=0.8, beta=0.5))
+    check_forward(echo, Case(T, H, x, r, "bf16", h, post=T % 2 == 0, pad=5, off=1, seed=1))
+
+
+@pytest.mark.parametrize("T,H", [(50, 512), (50, 515), (13, 4096)])
+@pytest.mark.parametrize("post", [True, False])
+@pytest.mark.parametrize("gate", [0, 1, 7, 50, 1 << 40])
+@pytest.mark.parametrize("has_r,weights", [(True, True), (False, True), (True, False)])
+def test_forward_forms(echo, T, H, post, gate, has_r, weights):
+    say("norm form", T, H, post, gate, has_r, weights)
+    check_forward(echo, Case(T, H, post=post, gate=gate, has_r=has_r, weights=weights, rho=-1.5, beta=0.25, pad=8))
+
+
+@pytest.mark.parametrize("H", [256, 1000, 1001, 4096, 17000])
+def test_forward_one_output_and_in_place(echo, H):
+    """r_out alone, h alone, and r_out over r give what the full call gives, bit for bit."""
+    say("norm outputs", H)
+    c = Case(21, H, r="f32", gate=4, rho=0.9)
+    r_out, h, _ = check_forward(echo, c)
+    alone = torch.empty_like(r_out)
+    echo.echo_block_norm(c.args(echo, r_out=alone))
+    only = torch.empty_like(h)
+    echo.echo_block_norm(c.args(echo, h=only))
+    c.r = c.r.clone()
+    place = torch.empty_like(h)
+    a = c.args(echo, r_out=c.r, h=place)
+    echo.echo_block_norm(a)
+    torch.cuda.synchronize()
+    same_bits(alone, r_out)
+    same_bits(only, h)
+    same_bits(place, h)
+    same_bits(c.r, r_out)
+
+
+@pytest.mark.parametrize("H", [128, 1001, 4096])
+@pytest.mark.parametrize("h", ["bf16", "i8"])
+def test_zero_and_non_finite_tokens(echo, H, h):
+    """A token of zeros gives zeros; an infinity or a NaN stays in its token."""
+    say("norm edge tokens", H, h)
+    c = Case(9, H, h=h, x="f32", r="f32")
+    clean = check_forward(echo, c)
+    c.x[2], c.r[2] = 0.0, 0.0
+    c.x[4, H // 2] = float("nan")
+    c.r[6, H - 1] = float("inf")
+    r_out, h_out = torch.empty_like(c.r), torch.empty(9, H, dtype=torch.int8 if h == "i8" else torch.bfloat16, device=DEV)
+    s = torch.empty(9, device=DEV)
+    echo.echo_block_norm(c.args(echo, r_out=r_out, h=h_out, h_scale=s if h == "i8" else None))
+    torch.cuda.synchronize()
+    keep = [0, 1, 3, 5, 7, 8]
+    same_bits(r_out[keep], clean[0][keep].contiguous())
+    same_bits(h_out[keep], clean[1][keep].contiguous())
+    assert not bool(r_out[2].any()) and not bool(h_out[2].any())
+    assert bool(torch.isnan(r_out[4]).all()) and bool(torch.isinf(r_out[6, H - 1]))
+    bad = s[[4, 6]] if h == "i8" else h_out[[4, 6]].float().sum(1)
+    assert bool(torch.isnan(bad).all())
+
+
+def test_no_tokens(echo):
+    x = torch.empty(0, 64, device=DEV)
+    echo.echo_block_norm(echo.make_norm_args(x, x, r_out=x, h=x))
+    dw = torch.full((2, 64), 7.0, device=DEV)
+    ws = torch.empty(max(16, echo.echo_block_norm_backward_workspace_bytes(0, 64)), dtype=torch.uint8, device=DEV)
+    echo.echo_block_norm_backward(echo.make_norm_args(x, x), echo.make_norm_grads(
+        dh=x, dr_out=x, dx=x, dr=x, dw_post=dw[0], dw_pre=dw[1], workspace=ws))
+    torch.cuda.synchronize()
+    assert not bool(dw.any())
+
+
+def test_forward_far_rows(echo):
+    """Rows past 2^31 elements."""
+    T, H, ld = 40, 1024, (1 << 31) // 39 + 8
+    say("norm far rows")
+    g = torch.Generator(device=DEV).manual_seed(1)
+    v = torch.randn(2, T, H, generator=g, device=DEV)
+    _, x = matrix(T, H, ld, torch.bfloat16, v[0])
+    _, r = matrix(T, H, ld, torch.bfloat16, v[1])
+    _, o = matrix(T, H, ld, torch.bfloat16, None)
+    h = torch.empty(T, H, device=DEV)
+    echo.echo_block_norm(echo.make_norm_args(x, r, r_out=o, h=h))
+    near, hn = torch.empty(T, H, dtype=torch.bfloat16, device=DEV), torch.empty(T, H, device=DEV)
+    echo.echo_block_norm(echo.make_norm_args(x.contiguous(), r.contiguous(), r_out=near, h=hn))
+    torch.cuda.synchronize()
+    same_bits(o, near)
+    same_bits(h, hn)
+
+
+# ---------------------------------------------------------------- backward --
+
+def run_backward(echo, c, dh=True, up=True, in_place=False, want=("dx", "dr", "dw_post", "dw_pre", "dgate")):
+    rows = -(-c.T // c.gate_tokens) if c.gate is not None else 0
+    got = dict(dx=c.out(c.kx), dr=c.out(c.kr), dw_post=matrix(1, c.H, c.H, torch.float32, None, c.off),
+               dw_pre=matrix(1, c.H, c.H, torch.float32, None, c.off), dgate=matrix(rows, c.H, c.H + c.pad, torch.float32, None, c.off))
+    skip = set() if c.post else {"dw_post"}
+    skip |= set() if c.gate is not None else {"dgate"}
+    skip |= set() if c.r is not None else {"dr"}
+    got = {k: v for k, v in got.items() if k in want and k not in skip}
+    dr_out = c.up
+    if in_place:
+        buf = torch.empty_like(got["dr"][0])
+        buf.copy_(got["dr"][0])
+        dr_out = torch.as_strided(got["dr"][0], c.up.shape, got["dr"][1].stride(), c.off)
+        dr_out.copy_(c.up)
+        got["dr"] = (got["dr"][0], dr_out)
+    need = echo.echo_block_norm_backward_workspace_bytes(c.T, c.H)
+    ws = torch.full((need + 64,), 77, dtype=torch.uint8, device=DEV)
+    views = {k: v[1][0] if k.startswith("dw") else v[1] for k, v in got.items()}
+    echo.echo_block_norm_backward(c.args(echo), echo.make_norm_grads(
+        dh=c.dh if dh else None, dr_out=dr_out if up else None, workspace=ws, workspace_bytes=need, **views))
+    torch.cuda.synchronize()
+    assert bool((ws[need:] == 77).all())
+    for k, (buf, v) in got.items():
+        untouched(buf, v)
+    return views
+
+
+def check_backward(echo, c, dh=True, up=True, **kw):
+    f = c.plain()
+    got = run_backward(echo, c, dh, up, **kw)
+    want, mag = ref.norm_backward(f, ref.f64(c.x), ref.f64(c.dh) if dh else None, ref.f64(c.up) if up else None,
+                                  ref.f64(c.gate), c.gate_tokens or 1, c.post, c.rho64, c.beta64)
+    for k, v in got.items():
+        tokens = {"dw_post": c.T, "dw_pre": c.T, "dgate": min(c.T, c.gate_tokens)}.get(k, 0)
+        within(v, want[k], ref.backward_eps(f, c.H, tokens) * mag[k] + 2.0 ** -140, k)
+    return got
+
+
+@pytest.mark.parametrize("T,H", SIZES)
+@pytest.mark.parametrize("x,r,h", list(itertools.product(["bf16", "f32"], ["bf16", "f32"], ["bf16", "f32"])))
+def test_backward_sizes_and_types(echo, T, H, x, r, h):
+    say("backward", T, H, x, r, h)
+    check_backward(echo, Case(T, H, x, r, "f32" if T % 2 else "bf16", h, gate=max(1, T // 2), rho=0.8, beta=0.5))
+    check_backward(echo, Case(T, H, x, r, "bf16", h, post=T % 2 == 0, pad=5, off=1, seed=1))
+
+
+@pytest.mark.parametrize("T,H", [(50, 512), (50, 515), (13, 4096)])
+@pytest.mark.parametrize("post", [True, False])
+@pytest.mark.parametrize("gate", [0, 1, 7, 50, 1 << 40])
+@pytest.mark.parametrize("has_r,weights", [(True, True), (False, True), (True, False)])
+def test_backward_forms(echo, T, H, post, gate, has_r, weights):
+    say("backward form", T, H, post, gate, has_r, weights)
+    check_backward(echo, Case(T, H, post=post, gate=gate, has_r=has_r, weights=weights, rho=-1.5, beta=0.25, pad=8))
+
+
+@pytest.mark.parametrize("T", [1000, 5000])
+@pytest.mark.parametrize("gate", [1, 3, 64, 601, 1500])
+@pytest.mark.parametrize("H", [256, 250])
+def test_backward_gate_rows_across_blocks(echo, T, gate, H):
+    """Gate rows shorter than, equal to and longer than any block's share of the tokens."""
+    say("backward gates", T, gate, H)
+    check_backward(echo, Case(T, H, gate=gate, beta=0.5))
+
+
+@pytest.mark.parametrize("H", [512, 1001, 17000])
+def test_backward_parts(echo, H):
+    """Either gradient alone coming in; any output left out; dr over dr_out; each bit for bit what the full call gives."""
+    say("backward parts", H)
+    c = Case(37, H, gate=10, r="f32", rho=0.9)
+    full = check_backward(echo, c)
+    check_backward(echo, c, dh=False)
+    check_backward(echo, c, up=False)
+    for want in (("dx",), ("dr",), ("dw_post", "dgate"), ("dw_pre",), ("dgate",), ("dx", "dr")):
+        got = run_backward(echo, c, want=want)
+        for k, v in got.items():
+            same_bits(v, full[k])
+    got = run_backward(echo, c, in_place=True)
+    for k, v in got.items():
+        same_bits(v, full[k])
+
+
+def test_backward_repeats_its_bits(echo):
+    say("backward repeats")
+    c = Case(3000, 768, gate=700)
+    a, b = run_backward(echo, c), run_backward(echo, c)
+    for k in a:
+        same_bits(a[k], b[k])
+
+
+@pytest.mark.parametrize("post,gate", [(True, 3), (False, 0)])
+def test_gradients_against_differences(echo, post, gate):
+    """<gradient, v> against a central difference of the loss along v in
+    float64 (step 1e-5: truncation about 1e-10, rounding about 1e-11); the
+    bound is the gradients' own, summed along v."""
+    say("differences", post, gate)
+    c = Case(12, 96, "f32", "f32", "f32", "f32", post=post, gate=gate, rho=0.8, beta=0.6)
+    f = c.plain()
+    got = run_backward(echo, c)
+    dh, up = ref.f64(c.dh), ref.f64(c.up)
+    _, mag = ref.norm_backward(f, ref.f64(c.x), dh, up, ref.f64(c.gate), gate or 1, post, c.rho64, c.beta64)
+    base = {k: ref.f64(getattr(c, k)) for k in ("x", "r", "w_post", "w_pre", "gate")}
+    rng = np.random.default_rng(5)
+    eps = float(np.float32(EPS))
+    for k, v in base.items():
+        if v is None:
+            continue
+        d = rng.standard_normal(v.shape)
+        side = []
+        for s in (1e-5, -1e-5):
+            w = dict(base)
+            w[k] = v + s * d
+            q = ref.norm_forward(w["x"], w["r"], w["w_post"], w["w_pre"], w["gate"], gate or 1, post, c.rho64, c.beta64, eps)
+            side.append((q["h"] * dh).sum() + (q["rn"] * up).sum())
+        want = (side[0] - side[1]) / 2e-5
+        have = float((ref.f64(got["d" + k]) * d).sum())
+        tol = ref.backward_eps(f, c.H, c.T) * float((mag["d" + k] * np.abs(d)).sum()) + 1e-6 * (1 + abs(want))
+        assert abs(have - want) <= tol, (k, have, want, tol)
+
+
+def test_forward_and_backward_in_a_graph(echo):
+    """Captured calls give the eager calls' bits on every replay."""
+    say("norm graph")
+    c = Case(300, 1024, gate=77)
+    r_out, h = torch.empty_like(c.r), torch.empty_like(c.x)
+    dx, dr = torch.empty_like(c.x), torch.empty_like(c.r)
+    dw, dg = torch.empty(2, 1024, device=DEV), torch.empty(4, 1024, device=DEV)
+    ws = torch.empty(echo.echo_block_norm_backward_workspace_bytes(300, 1024), dtype=torch.uint8, device=DEV)
+    fa, ba = c.args(echo, r_out=r_out, h=h), c.args(echo)
+    g = echo.make_norm_grads(dh=c.dh, dr_out=c.up, dx=dx, dr=dr, dw_post=dw[0], dw_pre=dw[1], dgate=dg, workspace=ws)
+
+    def both():
+        echo.echo_block_norm(fa)
+        echo.echo_block_norm_backward(ba, g)
+
+    both()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        both()
+    outs = (r_out, h, dx, dr, dw, dg)
+    for k in range(4):
+        c.x.copy_(torch.randn(300, 1024, device=DEV) * (k + 1))
+        for o in outs:
+            o.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [o.clone() for o in outs]
+        both()
+        torch.cuda.synchronize()
+        for p, q in zip(got, outs):
+            same_bits(p, q)
