@@ -33,13 +33,131 @@ bool bad_dim(int64_t v, int64_t most) { return v < 0 || v > most; }
 
 unsigned grid_of(int64_t items) { return (unsigned)(items < kMaxGrid ? items : kMaxGrid); }
 
+template <int G, int C, bool BF16>
+void quantize_go(const echo::QuantTokArgs& a, hipStream_t st)
+{
+    constexpr int kRows = echo::row_block<G>() / G;
+    const dim3 grid(grid_of((a.T + kRows - 1) / kRows)), block(echo::row_block<G>());
+    if (a.K % 8) hipLaunchKernelGGL((echo::quantize_tokens_kernel<G, C, BF16, true>), grid, block, 0, st, a);
+    else hipLaunchKernelGGL((echo::quantize_tokens_kernel<G, C, BF16, false>), grid, block, 0, st, a);
+}
+
+// The fewest threads that hold a token in two chunks each: a wave up to 1024
+// elements (no barrier), then a block.
+template <bool BF16>
+void quantize_sized(const echo::QuantTokArgs& a, hipStream_t st)
+{
+    if (a.K <= 512) quantize_go<64, 1, BF16>(a, st);
+    else if (a.K <= 1024) quantize_go<64, 2, BF16>(a, st);
+    else if (a.K <= 4096) quantize_go<256, 2, BF16>(a, st);
+    else if (a.K <= 16384) quantize_go<1024, 2, BF16>(a, st);
+    else hipLaunchKernelGGL(echo::quantize_long_tokens_kernel, dim3(grid_of(a.T)), dim3(echo::kBlock), 0, st, a);
+}
+
 void launch_quantize(const echo::QuantTokArgs& a, hipStream_t st)
 {
-    hipLaunchKernelGGL(echo::quantize_tokens_kernel, dim3(grid_of(a.T)), dim3(echo::kBlock), 0, st, a);
+    if (a.bf16) quantize_sized<true>(a, st);
+    else quantize_sized<false>(a, st);
 }
+
+// a launch's work-items are a 32-bit number
+bool grid_fits(int64_t blocks, int64_t threads) { return blocks * threads < (int64_t(1) << 32); }
+
+// NR 0: no form of this tile for rows that start anywhere
+template <int BM, int BN, int WM, int WN, int NS, int NR>
+void gemm_stage_go(echo::GemmI8Args& a, bool direct, hipStream_t st)
+{
+    a.tiles_m = (uint32_t)((a.M + BM - 1) / BM);
+    a.tiles_n = (uint32_t)((a.N + BN - 1) / BN);
+    const dim3 grid(a.tiles_m * a.tiles_n), block(64 * WM * WN);
+    if constexpr (NR > 0) {
+        if (!direct) {
+            hipLaunchKernelGGL((echo::gemm_i8_stage_kernel<BM, BN, WM, WN, 2, NR>), grid, block, 0, st, a);
+            return;
+        }
+    }
+    hipLaunchKernelGGL((echo::gemm_i8_stage_kernel<BM, BN, WM, WN, NS, 0>), grid, block, 0, st, a);
+}
+
+template <int MT, int XKIND, int FM, int C>
+void gemm_few_go(const echo::GemmI8Args& a, const void* xf, hipStream_t st)
+{
+    echo::FewArgs f;
+    f.g = a;
+    f.xf = xf;
+    f.pitch = echo::few_pitch(a.K);
+    const size_t parts = (size_t)echo::kFewWaves * MT * 1024, codes = XKIND ? (size_t)a.M * f.pitch : 0;
+    hipLaunchKernelGGL((echo::gemm_i8_few_kernel<MT, XKIND, FM, C>), dim3((unsigned)((a.N + 15) / 16)),
+                       dim3(echo::kFewThreads), parts > codes ? parts : codes, st, f);
+}
+
+// Layers that one launch quantizes and multiplies, while the tokens fit the
+// registers of gemm_i8_few_kernel: one token at N = K = 4096 takes 6.3 us, in
+// two launches 8.5; four tokens 7.9 and 9.0.
+constexpr int64_t kFusedTokens = 4, kFusedK = 2 * 8 * echo::kFewThreads;
+bool linear_fused(int64_t M, int64_t N, int64_t K)
+{
+    return M <= kFusedTokens && K <= kFusedK && grid_fits((N + 15) / 16, echo::kFewThreads);
+}
+
+template <int XKIND>
+void linear_fused_go(const echo::GemmI8Args& a, const void* x, hipStream_t st)
+{
+    const bool one = a.K <= kFusedK / 2;
+    if (a.M == 1) one ? gemm_few_go<1, XKIND, 1, 1>(a, x, st) : gemm_few_go<1, XKIND, 1, 2>(a, x, st);
+    else one ? gemm_few_go<1, XKIND, 4, 1>(a, x, st) : gemm_few_go<1, XKIND, 4, 2>(a, x, st);
+}
+
+// Tiles: one of the five sizes, by the estimated time of all rounds of tiles
+// over the CUs.  `us` is a full chip's round of that tile at K = 4096 as
+// measured, with direct loads and through registers; all grow alike with K.
+// The largest tile reads the least per product and wins where it fills the
+// chip (16384 x 4096 x 4096: 238 us, 270 with 128 x 256, 550 with 64 x 64);
+// small calls want a tile for every CU (100 x 4096 x 4096: 38 us with 256 x
+// 256, 9.6 with 64 x 64).  Through registers the largest tile spills and
+// gains nothing over the next one (88 us each at 4096 x 4096 x 3584).
+struct TileCost {
+    int bm, bn;
+    float us[2];
+};
+constexpr TileCost kTiles[] = {{256, 256, {61.0f, 0.0f}},
+                               {128, 256, {37.0f, 51.0f}},
+                               {128, 128, {24.0f, 31.5f}},
+                               {64, 128, {14.9f, 25.0f}},
+                               {64, 64, {9.6f, 15.8f}}};
+constexpr int64_t kCus = 256;
 
 void launch_gemm_i8(echo::GemmI8Args& a, hipStream_t st)
 {
+    // Up to 32 tokens: the weight streams past the tokens, no tiles (27 x 4096
+    // x 3584: 8.2 us, 8.8 in 64 x 64 tiles; 16 x 1000 x 8192: 9.8 and 14.7;
+    // from 33 on the tiles win: 48 x 4096 x 4096: 12.2 and 9.6).
+    if (a.M <= 32 && grid_fits((a.N + 15) / 16, echo::kFewThreads)) {
+        if (a.M <= 16) gemm_few_go<1, 0, 1, 1>(a, nullptr, st);
+        else gemm_few_go<2, 0, 1, 1>(a, nullptr, st);
+        return;
+    }
+    const bool direct = aligned16(a.x) && aligned16(a.w) && a.ldx % 16 == 0 && a.ldw % 16 == 0;
+    int best = -1;
+    float least = 0.0f;
+    for (int i = 0; i < 5; ++i) {
+        const int64_t tiles = ((a.M + kTiles[i].bm - 1) / kTiles[i].bm) * ((a.N + kTiles[i].bn - 1) / kTiles[i].bn);
+        const float t = (float)((tiles + kCus - 1) / kCus) * kTiles[i].us[direct ? 0 : 1];
+        if (t > 0.0f && grid_fits(tiles, 512) && (best < 0 || t < least)) {
+            best = i;
+            least = t;
+        }
+    }
+    if (a.ldx >= echo::kI8StageLd || a.ldw >= echo::kI8StageLd) best = -1;
+    switch (best) {
+    case 0: return gemm_stage_go<256, 256, 2, 4, 2, 0>(a, direct, st);
+    case 1: return gemm_stage_go<128, 256, 2, 4, 3, 2>(a, direct, st);
+    case 2: return gemm_stage_go<128, 128, 2, 4, 4, 2>(a, direct, st);
+    case 3: return gemm_stage_go<64, 128, 2, 2, 4, 2>(a, direct, st);
+    case 4: return gemm_stage_go<64, 64, 2, 2, 4, 4>(a, direct, st);
+    default: break;
+    }
+    // rows too far apart for 32-bit offsets, or more tiles than a launch holds
     a.tiles_m = (uint32_t)((a.M + 63) / 64);
     a.tiles_n = (uint32_t)((a.N + 63) / 64);
     hipLaunchKernelGGL(echo::gemm_i8_tile_kernel, dim3(grid_of((int64_t)a.tiles_m * a.tiles_n)), dim3(echo::kBlock), 0,
@@ -60,19 +178,21 @@ int check_product(const int8_t* w, int64_t ldw, const float* sw, const float* bi
     return ECHO_OK;
 }
 
+// codes of the linear layer's tokens: rows of a multiple of 16, then the scales
+int64_t codes_ld(int64_t K) { return (K + 15) / 16 * 16; }
+
 echo::GemmI8Args gemm_args(const int8_t* x, int64_t ldx, const float* sx, const int8_t* w, int64_t ldw, const float* sw,
                            const float* bias, int64_t M, int64_t N, int64_t K, void* y, int64_t ldy, int y_dtype)
 {
     echo::GemmI8Args a;
     std::memset(&a, 0, sizeof(a));
     a.x = x; a.w = w; a.sx = sx; a.sw = sw; a.bias = bias; a.y = y;
-    a.M = M; a.N = N; a.ldx = ldx; a.ldw = ldw; a.ldy = ldy;
+    a.M = M; a.N = N; a.ldy = ldy;
+    a.ldx = M > 1 ? ldx : codes_ld(K);     // a single row's ld is not the caller's to set
+    a.ldw = N > 1 ? ldw : codes_ld(K);
     a.K = (int)K; a.bf16 = y_dtype == ECHO_BF16;
     return a;
 }
-
-// codes of the linear layer's tokens: rows of a multiple of 16, then the scales
-int64_t codes_ld(int64_t K) { return (K + 15) / 16 * 16; }
 
 // ------------------------------------------------------------------ norms --
 
@@ -168,7 +288,7 @@ int echo_gemm_int8(const int8_t* x, int64_t ldx, const float* sx, const int8_t* 
 size_t echo_linear_int8_workspace_bytes(int64_t M, int64_t N, int64_t K)
 {
     if (bad_dim(M, kMaxRows) || bad_dim(N, kMaxRows) || bad_dim(K, echo::kI8MaxK)) return 0;
-    return (size_t)(M * codes_ld(K) + 4 * M);
+    return linear_fused(M, N, K) ? 0 : (size_t)(M * codes_ld(K) + 4 * M);
 }
 
 int echo_linear_int8(const void* x, int64_t ldx, int x_dtype, const int8_t* w, int64_t ldw, const float* sw,
@@ -182,9 +302,16 @@ int echo_linear_int8(const void* x, int64_t ldx, int x_dtype, const int8_t* w, i
     if (M == 0 || N == 0) return ECHO_OK;
     if (K && !x) return ECHO_EINVAL;
     if (!aligned_elem(x, x_dtype)) return ECHO_EALIGN;
-    if (!workspace || workspace_bytes < echo_linear_int8_workspace_bytes(M, N, K)) return ECHO_EINVAL;
+    const size_t need = echo_linear_int8_workspace_bytes(M, N, K);
+    if (need && (!workspace || workspace_bytes < need)) return ECHO_EINVAL;
     if (!aligned16(workspace)) return ECHO_EALIGN;
     const hipStream_t st = (hipStream_t)stream;
+    if (linear_fused(M, N, K)) {
+        const echo::GemmI8Args a = gemm_args(nullptr, ldx, nullptr, w, ldw, sw, bias, M, N, K, y, ldy, y_dtype);
+        if (x_dtype == ECHO_BF16) linear_fused_go<1>(a, x, st);
+        else linear_fused_go<2>(a, x, st);
+        return check_launch();
+    }
     const int64_t ldq = codes_ld(K);
     int8_t* q = (int8_t*)workspace;
     float* s = (float*)(q + M * ldq);

@@ -359,7 +359,8 @@ size_t echo_noalloc_scratch_bytes(void);
  * Conventions, beside those above:
  *  - A matrix is rows of contiguous elements at a distance of ld elements
  *    (ld >= the row's length; a single row's ld is not used).  Nothing
- *    outside the rows is read or written.
+ *    outside the rows is written, and no aligned 4-byte word that holds none
+ *    of a row is read.
  *  - Pointers need the alignment of their element type only (workspaces 16
  *    bytes); where the base and ld of every matrix of a call are multiples of
  *    16 bytes the call is fastest.
