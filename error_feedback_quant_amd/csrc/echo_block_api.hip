@@ -242,12 +242,52 @@ echo::NormArgs norm_args(const echo_norm_args& a)
     n.x = a.x; n.r = a.r; n.w_post = a.w_post; n.w_pre = a.w_pre; n.gate = a.gate;
     n.r_out = a.r_out; n.h = a.h; n.h_scale = a.h_scale;
     n.T = a.T; n.ld_x = a.ld_x; n.ld_r = a.ld_r; n.ld_r_out = a.ld_r_out; n.ld_h = a.ld_h; n.ld_gate = a.ld_gate;
-    n.gate_tokens = a.gate_tokens;
+    n.gate_tokens = (uint32_t)(a.gate_tokens < a.T ? a.gate_tokens : a.T);
     n.H = (int)a.H;
     n.x_bf16 = a.x_dtype == ECHO_BF16; n.r_bf16 = a.r_dtype == ECHO_BF16; n.w_bf16 = a.w_dtype == ECHO_BF16;
     n.h_kind = a.h_dtype; n.post = a.post;
     n.eps = a.eps; n.rho = a.res_scale; n.beta = a.block_scale;
     return n;
+}
+
+// f(G, C) for the threads and chunks that hold a row of H elements: a wave up
+// to 1024 (no barrier), then whole blocks.  False: too long for registers.
+template <typename F>
+bool with_row_shape(int64_t H, F f)
+{
+    using std::integral_constant;
+    if (H <= 512) f(integral_constant<int, 64>{}, integral_constant<int, 1>{});
+    else if (H <= 1024) f(integral_constant<int, 64>{}, integral_constant<int, 2>{});
+    else if (H <= 2048) f(integral_constant<int, 256>{}, integral_constant<int, 1>{});
+    else if (H <= 4096) f(integral_constant<int, 256>{}, integral_constant<int, 2>{});
+    else if (H <= 8192) f(integral_constant<int, 512>{}, integral_constant<int, 2>{});
+    else if (H <= 16384) f(integral_constant<int, 1024>{}, integral_constant<int, 2>{});
+    else return false;
+    return true;
+}
+
+// blocks of a forward launch: enough to fill the chip, each for several tokens
+constexpr int64_t kNormBlocks = 8 * kCus;
+
+template <int G, int C, bool XB, bool RB>
+void block_norm_go(const echo::NormArgs& a, hipStream_t st)
+{
+    constexpr int kRows = echo::row_block<G>() / G;
+    const int64_t blocks = (a.T + kRows - 1) / kRows;
+    const dim3 grid((unsigned)(blocks < kNormBlocks ? blocks : kNormBlocks)), block(echo::row_block<G>());
+    if (a.H % 8) hipLaunchKernelGGL((echo::block_norm_kernel<G, C, XB, RB, true>), grid, block, 0, st, a);
+    else hipLaunchKernelGGL((echo::block_norm_kernel<G, C, XB, RB, false>), grid, block, 0, st, a);
+}
+
+void launch_block_norm(const echo::NormArgs& a, hipStream_t st)
+{
+    const bool held = with_row_shape(a.H, [&](auto g, auto c) {
+        constexpr int G = decltype(g)::value, C = decltype(c)::value;
+        if (a.x_bf16) a.r_bf16 ? block_norm_go<G, C, true, true>(a, st) : block_norm_go<G, C, true, false>(a, st);
+        else a.r_bf16 ? block_norm_go<G, C, false, true>(a, st) : block_norm_go<G, C, false, false>(a, st);
+    });
+    if (!held)
+        hipLaunchKernelGGL(echo::block_norm_any_kernel, dim3(grid_of(a.T)), dim3(echo::kBlock), 0, st, a);
 }
 
 }  // namespace
@@ -331,7 +371,7 @@ int echo_block_norm(const echo_norm_args* p, void* stream)
     const int rc = check_norm(p, false);
     if (rc || p->T == 0 || p->H == 0) return rc;
     const echo::NormArgs a = norm_args(*p);
-    hipLaunchKernelGGL(echo::block_norm_any_kernel, dim3(grid_of(a.T)), dim3(echo::kBlock), 0, (hipStream_t)stream, a);
+    launch_block_norm(a, (hipStream_t)stream);
     return check_launch();
 }
 

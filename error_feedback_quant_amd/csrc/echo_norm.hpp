@@ -32,7 +32,8 @@ struct NormArgs {
     void* r_out;            // nullable
     void* h;                // nullable
     float* h_scale;         // [T], 8-bit h only
-    int64_t T, ld_x, ld_r, ld_r_out, ld_h, ld_gate, gate_tokens;
+    int64_t T, ld_x, ld_r, ld_r_out, ld_h, ld_gate;
+    uint32_t gate_tokens;   // at most T
     int H;
     int x_bf16, r_bf16, w_bf16, h_kind;    // h_kind: an echo_dtype
     int post;
@@ -83,10 +84,120 @@ __device__ __forceinline__ NormElem norm_elem(const NormArgs& a, int64_t t, int 
     e.n_x = e.x * kx;
     e.w_post = a.w_post ? ld_elem(a.w_post, a.w_bf16, c) : 1.0f;
     e.z = a.post ? e.n_x * e.w_post : e.x;
-    e.g = a.gate ? ld_elem(a.gate, a.w_bf16, (t / a.gate_tokens) * a.ld_gate + c) : 1.0f;
+    e.g = a.gate ? ld_elem(a.gate, a.w_bf16, (int64_t)((uint32_t)t / a.gate_tokens) * a.ld_gate + c) : 1.0f;
     const float r = a.r ? ld_elem(a.r, a.r_bf16, t * a.ld_r + c) : 0.0f;
     e.r = a.rho * r + a.beta * (e.g * e.z);
     return e;
+}
+
+// 8 weights (or gate values) of a row from k on; ones where there are none
+template <bool TAIL>
+__device__ __forceinline__ void ld_weights8(const void* base, int bf16, int64_t row, int k, int H, float (&w)[8])
+{
+    if (!base) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = 1.0f;
+    } else if (bf16) {
+        const Raw8<true> r = ld_raw8<true, TAIL>(base, row, k, H);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = raw_get(r, e);
+    } else {
+        const Raw8<false> r = ld_raw8<false, TAIL>(base, row, k, H);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = raw_get(r, e);
+    }
+}
+
+// A token held in registers: G threads, C chunks of 8 elements each, every
+// byte moved once.  The weights stay in registers over the tokens of a group
+// of threads, and so does the gate while its row lasts.
+template <int G, int C, bool XB, bool RB, bool TAIL>
+__global__ __launch_bounds__(row_block<G>()) void block_norm_kernel(const NormArgs a)
+{
+    __shared__ float red[G > 64 ? 2 * G / 64 : 1];
+    constexpr int kRows = row_block<G>() / G;
+    const int g = threadIdx.x % G;
+    int64_t t = (int64_t)blockIdx.x * kRows + threadIdx.x / G;
+    if constexpr (G == 64) t = __builtin_amdgcn_readfirstlane((int)t);
+    const int64_t step = (int64_t)gridDim.x * kRows;
+    float w_post[C][8], w_pre[C][8], gate[C][8];
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+        ld_weights8<TAIL>(a.w_post, a.w_bf16, 0, 8 * (g + G * j), a.H, w_post[j]);
+        ld_weights8<TAIL>(a.w_pre, a.w_bf16, 0, 8 * (g + G * j), a.H, w_pre[j]);
+        ld_weights8<TAIL>(nullptr, 0, 0, 0, 0, gate[j]);
+    }
+    uint32_t gate_row = ~0u;
+    int turn = 0;
+    for (; t < a.T; t += step) {
+        Raw8<XB> x[C];
+        Raw8<RB> r[C];
+#pragma unroll
+        for (int j = 0; j < C; ++j) {
+            const int k = 8 * (g + G * j);
+            x[j] = ld_raw8<XB, TAIL>(a.x, t * a.ld_x, k, a.H);
+            r[j] = ld_raw8<RB, TAIL>(a.r, t * a.ld_r, k, a.r ? a.H : 0);
+        }
+        if (a.gate) {
+            const uint32_t row = (uint32_t)t / a.gate_tokens;
+            if (row != gate_row) {
+#pragma unroll
+                for (int j = 0; j < C; ++j)
+                    ld_weights8<TAIL>(a.gate, a.w_bf16, (int64_t)row * a.ld_gate, 8 * (g + G * j), a.H, gate[j]);
+                gate_row = row;
+            }
+        }
+        float kx = 1.0f;
+        if (a.post) {
+            float s = 0.0f;
+#pragma unroll
+            for (int j = 0; j < C; ++j)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) s = fmaf(raw_get(x[j], e), raw_get(x[j], e), s);
+            kx = norm_factor(row_sum<G>(s, red, turn++), a.H, a.eps);
+        }
+        float v[C][8];
+        float s = 0.0f;
+#pragma unroll
+        for (int j = 0; j < C; ++j) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float z = raw_get(x[j], e) * kx * w_post[j][e];
+                v[j][e] = a.rho * raw_get(r[j], e) + a.beta * (gate[j][e] * z);
+                s = fmaf(v[j][e], v[j][e], s);
+            }
+            if (a.r_out) st_row8<RB, TAIL>(a.r_out, t * a.ld_r_out, 8 * (g + G * j), a.H, v[j]);
+        }
+        if (!a.h) continue;
+        const float kr = norm_factor(row_sum<G>(s, red, turn++), a.H, a.eps);
+#pragma unroll
+        for (int j = 0; j < C; ++j)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[j][e] = v[j][e] * kr * w_pre[j][e];
+        if (a.h_kind == ECHO_I8) {
+            uint32_t m = 0;
+#pragma unroll
+            for (int j = 0; j < C; ++j)
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (!TAIL || 8 * (g + G * j) + e < a.H) m = max(m, abs_bits(v[j][e]));
+            const TokenScale q = token_scale(row_max_u32<G>(m, red, turn++));
+            if (g == 0) a.h_scale[t] = q.scale;
+#pragma unroll
+            for (int j = 0; j < C; ++j) {
+                int c[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) c[e] = token_code(v[j][e], q.inv);
+                st_codes8<TAIL>((int8_t*)a.h, t * a.ld_h, 8 * (g + G * j), a.H, c);
+            }
+        } else if (a.h_kind == ECHO_BF16) {
+#pragma unroll
+            for (int j = 0; j < C; ++j) st_row8<true, TAIL>(a.h, t * a.ld_h, 8 * (g + G * j), a.H, v[j]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < C; ++j) st_row8<false, TAIL>(a.h, t * a.ld_h, 8 * (g + G * j), a.H, v[j]);
+        }
+    }
 }
 
 // One block per token of any width; the row is read again in each pass.
@@ -231,9 +342,9 @@ __global__ __launch_bounds__(kBlock) void norm_bwd_gate_kernel(const NormBwdArgs
     const int c = blockIdx.x * kBlock + threadIdx.x;
     if (c >= a.H) return;
     for (int64_t g = blockIdx.y; g < rows; g += gridDim.y) {
-        const int64_t t1 = g + 1 < rows ? (g + 1) * a.gate_tokens : a.T;
+        const int64_t t1 = min(a.T, (g + 1) * (int64_t)a.gate_tokens);
         float s = 0.0f;
-        for (int64_t t = g * a.gate_tokens; t < t1; ++t) {
+        for (int64_t t = g * (int64_t)a.gate_tokens; t < t1; ++t) {
             const f32x4 st = *(const f32x4*)(b.stats + 4 * t);
             const NormGrad v = norm_grad(b, t, c, st.x, st.y, st.z);
             s += a.beta * v.d * v.e.z;
