@@ -197,11 +197,77 @@ echo::GemmI8Args gemm_args(const int8_t* x, int64_t ldx, const float* sx, const 
 // ------------------------------------------------------------------ norms --
 
 constexpr int64_t kMaxWidth = int64_t(1) << 30;
+constexpr int64_t kBwdWidth = 8192;                 // rows whose backward pass fits a block's registers
+size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
+
+// f(G, C) for the threads and chunks that hold a row of H elements: a wave up
+// to 1024 (no barrier), then whole blocks.  False: too long for registers.
+template <typename F>
+bool with_row_shape(int64_t H, F f)
+{
+    using std::integral_constant;
+    if (H <= 512) f(integral_constant<int, 64>{}, integral_constant<int, 1>{});
+    else if (H <= 1024) f(integral_constant<int, 64>{}, integral_constant<int, 2>{});
+    else if (H <= 2048) f(integral_constant<int, 256>{}, integral_constant<int, 1>{});
+    else if (H <= 4096) f(integral_constant<int, 256>{}, integral_constant<int, 2>{});
+    else if (H <= 8192) f(integral_constant<int, 512>{}, integral_constant<int, 2>{});
+    else if (H <= 16384) f(integral_constant<int, 1024>{}, integral_constant<int, 2>{});
+    else return false;
+    return true;
+}
+
+// The same for the backward pass, whose sums and weights take three times the
+// registers: one chunk a thread.
+template <typename F>
+bool with_bwd_shape(int64_t H, F f)
+{
+    using std::integral_constant;
+    if (H <= 512) f(integral_constant<int, 64>{}, integral_constant<int, 1>{});
+    else if (H <= 1024) f(integral_constant<int, 128>{}, integral_constant<int, 1>{});
+    else if (H <= 2048) f(integral_constant<int, 256>{}, integral_constant<int, 1>{});
+    else if (H <= 4096) f(integral_constant<int, 512>{}, integral_constant<int, 1>{});
+    else if (H <= kBwdWidth) f(integral_constant<int, 1024>{}, integral_constant<int, 1>{});
+    else return false;
+    return true;
+}
+
+// How a backward pass is split, and where its parts lie in the workspace.
+struct BwdPlan {
+    int64_t blocks;          // of the row kernel; chunks of tokens for long rows
+    int64_t per, groups;     // tokens of a group, groups that have any
+    int group_size;          // groups of a block
+    size_t stats, part, gpart, total;
+};
+constexpr int64_t kBwdWaves = 8;
 constexpr int64_t kMaxChunks = 256;
 
-int norm_chunks(int64_t T) { return (int)(T / 16 < 1 ? 1 : (T / 16 > kMaxChunks ? kMaxChunks : T / 16)); }
-
-size_t norm_stats_bytes(int64_t T) { return (size_t)(T * 16); }
+BwdPlan bwd_plan(int64_t T, int64_t H)
+{
+    BwdPlan p = {};
+    if (H > kBwdWidth) {
+        p.blocks = T / 16 < 1 ? 1 : (T / 16 > kMaxChunks ? kMaxChunks : T / 16);
+        p.part = align256((size_t)(T * 16));
+        p.total = p.part + (size_t)(p.blocks * 2 * H * 4);
+        return p;
+    }
+    int threads = 0;
+    with_bwd_shape(H, [&](auto g, auto) {
+        threads = echo::row_block<decltype(g)::value>();
+        p.group_size = threads / decltype(g)::value;
+    });
+    // two tokens a group at least, and 8 waves on a CU (more do not fit the
+    // registers: 12 took 320 us at 131072 x 1024, 8 take 302) or one block
+    int64_t most = kBwdWaves * 64 * kCus / threads;
+    if (most < kCus) most = kCus;
+    most *= p.group_size;
+    const int64_t groups = (T + 1) / 2 < most ? (T + 1) / 2 : most;
+    p.per = groups ? (T + groups - 1) / groups : 1;
+    p.groups = (T + p.per - 1) / p.per;
+    p.blocks = (p.groups + p.group_size - 1) / p.group_size;
+    p.gpart = align256((size_t)(p.blocks * 2 * H * 4));
+    p.total = p.gpart + (size_t)(p.groups * 2 * H * 4);
+    return p;
+}
 
 int check_norm(const echo_norm_args* p, bool backward)
 {
@@ -250,31 +316,22 @@ echo::NormArgs norm_args(const echo_norm_args& a)
     return n;
 }
 
-// f(G, C) for the threads and chunks that hold a row of H elements: a wave up
-// to 1024 (no barrier), then whole blocks.  False: too long for registers.
-template <typename F>
-bool with_row_shape(int64_t H, F f)
-{
-    using std::integral_constant;
-    if (H <= 512) f(integral_constant<int, 64>{}, integral_constant<int, 1>{});
-    else if (H <= 1024) f(integral_constant<int, 64>{}, integral_constant<int, 2>{});
-    else if (H <= 2048) f(integral_constant<int, 256>{}, integral_constant<int, 1>{});
-    else if (H <= 4096) f(integral_constant<int, 256>{}, integral_constant<int, 2>{});
-    else if (H <= 8192) f(integral_constant<int, 512>{}, integral_constant<int, 2>{});
-    else if (H <= 16384) f(integral_constant<int, 1024>{}, integral_constant<int, 2>{});
-    else return false;
-    return true;
-}
-
-// blocks of a forward launch: enough to fill the chip, each for several tokens
-constexpr int64_t kNormBlocks = 8 * kCus;
+// Blocks of a forward launch: those that the chip holds at once, each walking
+// over its tokens with the weights in registers (2048 x 4096 in 23.5 us, 26.7
+// with a block for each token), or, past kNormRounds rounds of them and
+// without a gate, a block for each token, which keeps the chip on one stretch
+// of memory (131072 x 1024: 182 us, 202 walking; with a gate to load for each
+// token 196, 189 walking; rows of 8192, whose weights weigh more: 104 and 97).
+constexpr int64_t kNormThreads = 1024 * kCus, kNormRounds = 8;
 
 template <int G, int C, bool XB, bool RB>
 void block_norm_go(const echo::NormArgs& a, hipStream_t st)
 {
-    constexpr int kRows = echo::row_block<G>() / G;
-    const int64_t blocks = (a.T + kRows - 1) / kRows;
-    const dim3 grid((unsigned)(blocks < kNormBlocks ? blocks : kNormBlocks)), block(echo::row_block<G>());
+    constexpr int kThreads = echo::row_block<G>(), kRows = kThreads / G;
+    int64_t blocks = (a.T + kRows - 1) / kRows;
+    const int64_t held = kNormThreads / kThreads;
+    if (blocks > held && (a.gate || G > 256 || blocks <= kNormRounds * held)) blocks = held;
+    const dim3 grid(grid_of(blocks)), block(kThreads);
     if (a.H % 8) hipLaunchKernelGGL((echo::block_norm_kernel<G, C, XB, RB, true>), grid, block, 0, st, a);
     else hipLaunchKernelGGL((echo::block_norm_kernel<G, C, XB, RB, false>), grid, block, 0, st, a);
 }
@@ -288,6 +345,67 @@ void launch_block_norm(const echo::NormArgs& a, hipStream_t st)
     });
     if (!held)
         hipLaunchKernelGGL(echo::block_norm_any_kernel, dim3(grid_of(a.T)), dim3(echo::kBlock), 0, st, a);
+}
+
+template <int G, int C, bool XB, bool RB>
+void block_norm_bwd_go(const echo::NormBwdArgs& b, hipStream_t st)
+{
+    const dim3 grid((unsigned)b.chunks), block(echo::row_block<G>());
+    auto go = [&](auto hb, auto tail) {
+        hipLaunchKernelGGL((echo::block_norm_bwd_kernel<G, C, XB, RB, decltype(hb)::value, decltype(tail)::value>), grid,
+                           block, 0, st, b);
+    };
+    if (b.f.H % 8) b.dh_bf16 ? go(std::true_type{}, std::true_type{}) : go(std::false_type{}, std::true_type{});
+    else b.dh_bf16 ? go(std::true_type{}, std::false_type{}) : go(std::false_type{}, std::false_type{});
+}
+
+int launch_block_norm_bwd(const echo::NormBwdArgs& b, const BwdPlan& plan, hipStream_t st)
+{
+    const echo::NormArgs& a = b.f;
+    int e;
+    if (a.T > 0) {
+        with_bwd_shape(a.H, [&](auto g, auto c) {
+            constexpr int G = decltype(g)::value, C = decltype(c)::value;
+            if (a.x_bf16) a.r_bf16 ? block_norm_bwd_go<G, C, true, true>(b, st) : block_norm_bwd_go<G, C, true, false>(b, st);
+            else a.r_bf16 ? block_norm_bwd_go<G, C, false, true>(b, st) : block_norm_bwd_go<G, C, false, false>(b, st);
+        });
+        if ((e = check_launch())) return e;
+    }
+    // gate rows that groups share; with a gate for each token there are none
+    int64_t rows = b.dgate && a.gate_tokens > 1 ? (plan.groups < b.gate_rows ? plan.groups : b.gate_rows) : 0;
+    if (rows > 4096) rows = 4096;
+    if (!b.dw_post && !b.dw_pre && !rows) return ECHO_OK;
+    hipLaunchKernelGGL(echo::norm_bwd_sum_kernel, dim3((unsigned)((a.H + 63) / 64), (unsigned)(2 + rows)),
+                       dim3(64 * echo::kSumWaves), 0, st, b, plan.group_size);
+    return check_launch();
+}
+
+// rows too long for registers: their statistics, then the sums by columns, then the rows' gradients
+int launch_long_norm_bwd(const echo::NormBwdArgs& b, hipStream_t st)
+{
+    const echo::NormArgs& a = b.f;
+    const unsigned cols = (unsigned)((a.H + echo::kBlock - 1) / echo::kBlock);
+    const dim3 block(echo::kBlock);
+    int e;
+    if (a.T > 0) {
+        hipLaunchKernelGGL(echo::norm_bwd_stats_kernel, dim3(grid_of(a.T)), block, 0, st, b);
+        if ((e = check_launch())) return e;
+    }
+    if (b.dw_post || b.dw_pre) {
+        hipLaunchKernelGGL(echo::norm_bwd_weights_kernel, dim3(cols, (unsigned)b.chunks), block, 0, st, b);
+        if ((e = check_launch())) return e;
+        hipLaunchKernelGGL(echo::norm_bwd_weights_sum_kernel, dim3(cols), block, 0, st, b);
+        if ((e = check_launch())) return e;
+    }
+    if (b.dgate && b.gate_rows > 0) {
+        hipLaunchKernelGGL(echo::norm_bwd_gate_kernel, dim3(cols, b.gate_rows < 32768 ? b.gate_rows : 32768), block, 0, st, b);
+        if ((e = check_launch())) return e;
+    }
+    if (a.T > 0 && (b.dx || b.dr)) {
+        hipLaunchKernelGGL(echo::norm_bwd_apply_kernel, dim3(grid_of(a.T)), block, 0, st, b);
+        if ((e = check_launch())) return e;
+    }
+    return ECHO_OK;
 }
 
 }  // namespace
@@ -378,7 +496,7 @@ int echo_block_norm(const echo_norm_args* p, void* stream)
 size_t echo_block_norm_backward_workspace_bytes(int64_t T, int64_t H)
 {
     if (bad_dim(T, kMaxRows) || bad_dim(H, kMaxWidth)) return 0;
-    return norm_stats_bytes(T) + (size_t)norm_chunks(T) * 2 * (size_t)H * 4;
+    return bwd_plan(T, H).total;
 }
 
 int echo_block_norm_backward(const echo_norm_args* p, const echo_norm_grads* gp, void* stream)
@@ -401,7 +519,8 @@ int echo_block_norm_backward(const echo_norm_args* p, const echo_norm_grads* gp,
         (g.dx && !aligned_elem(g.dx, p->x_dtype)) || (g.dr && !aligned_elem(g.dr, p->r_dtype)) ||
         !aligned_to(g.dw_post, 4) || !aligned_to(g.dw_pre, 4) || !aligned_to(g.dgate, 4))
         return ECHO_EALIGN;
-    if (!g.workspace || g.workspace_bytes < echo_block_norm_backward_workspace_bytes(T, H)) return ECHO_EINVAL;
+    const size_t need = echo_block_norm_backward_workspace_bytes(T, H);
+    if (need && (!g.workspace || g.workspace_bytes < need)) return ECHO_EINVAL;
     if (!aligned16(g.workspace)) return ECHO_EALIGN;
     echo::NormBwdArgs b;
     std::memset(&b, 0, sizeof(b));
@@ -410,33 +529,18 @@ int echo_block_norm_backward(const echo_norm_args* p, const echo_norm_grads* gp,
     b.dw_post = g.dw_post; b.dw_pre = g.dw_pre; b.dgate = g.dgate;
     b.ld_dh = g.ld_dh; b.ld_dr_out = g.ld_dr_out; b.ld_dx = g.ld_dx; b.ld_dr = g.ld_dr; b.ld_dgate = g.ld_dgate;
     b.dh_bf16 = g.dh_dtype == ECHO_BF16;
-    b.stats = (float*)g.workspace;
-    b.part = (float*)((uint8_t*)g.workspace + norm_stats_bytes(T));
-    b.chunks = norm_chunks(T);
+    const BwdPlan plan = bwd_plan(T, H);
+    uint8_t* ws = (uint8_t*)g.workspace;
+    b.stats = (float*)(ws + plan.stats);
+    b.part = (float*)(ws + plan.part);
+    b.gpart = (float*)(ws + plan.gpart);
+    b.chunks = T > 0 ? (int)plan.blocks : 0;
+    b.per = (uint32_t)plan.per;
+    b.groups = (uint32_t)plan.groups;
+    b.gate_rows = (uint32_t)rows;
+    b.spread = rows <= 1;
     const hipStream_t st = (hipStream_t)stream;
-    const unsigned cols = (unsigned)((H + echo::kBlock - 1) / echo::kBlock);
-    const dim3 block(echo::kBlock);
-    int e;
-    if (T > 0) {
-        hipLaunchKernelGGL(echo::norm_bwd_stats_kernel, dim3(grid_of(T)), block, 0, st, b);
-        if ((e = check_launch())) return e;
-    }
-    if (g.dw_post || g.dw_pre) {
-        hipLaunchKernelGGL(echo::norm_bwd_weights_kernel, dim3(cols, (unsigned)b.chunks), block, 0, st, b);
-        if ((e = check_launch())) return e;
-        hipLaunchKernelGGL(echo::norm_bwd_weights_sum_kernel, dim3(cols), block, 0, st, b);
-        if ((e = check_launch())) return e;
-    }
-    if (g.dgate && rows > 0) {
-        hipLaunchKernelGGL(echo::norm_bwd_gate_kernel, dim3(cols, (unsigned)(rows < 32768 ? rows : 32768)), block, 0, st,
-                           b, rows);
-        if ((e = check_launch())) return e;
-    }
-    if (T > 0 && (g.dx || g.dr)) {
-        hipLaunchKernelGGL(echo::norm_bwd_apply_kernel, dim3(grid_of(T)), block, 0, st, b);
-        if ((e = check_launch())) return e;
-    }
-    return ECHO_OK;
+    return H > kBwdWidth ? launch_long_norm_bwd(b, st) : launch_block_norm_bwd(b, plan, st);
 }
 
 }  // extern "C"

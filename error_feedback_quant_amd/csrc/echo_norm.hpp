@@ -51,9 +51,14 @@ struct NormBwdArgs {
     float* dgate;
     int64_t ld_dh, ld_dr_out, ld_dx, ld_dr, ld_dgate;
     int dh_bf16;
-    float* stats;           // [T][4]: k_x, k_r, mean(dh w_pre n_r), mean(dz w_post n_x)
-    float* part;            // [chunks][2][H] partial dw_post, dw_pre
-    int chunks;
+    float* stats;           // long rows: [T][4]: k_x, k_r, mean(dh w_pre n_r), mean(dz w_post n_x)
+    float* part;            // [blocks or chunks][2][H] partial dw_post, dw_pre
+    float* gpart;           // [groups][2][H] partial dgate of a group's first and last gate row
+    int chunks;             // blocks of the row kernel, or chunks of tokens
+    uint32_t per;           // tokens of a group
+    uint32_t groups;        // groups that have tokens
+    int spread;             // one gate row (or none): tokens go round the groups
+    uint32_t gate_rows;
 };
 
 __device__ __forceinline__ float block_sum(float v, float* red)
@@ -108,6 +113,17 @@ __device__ __forceinline__ void ld_weights8(const void* base, int bf16, int64_t 
     }
 }
 
+// beta gate w_post of 8 columns, what a normed x is multiplied by
+template <bool TAIL>
+__device__ __forceinline__ void ld_branch8(const NormArgs& a, const void* gate, int64_t row, int k, float (&w)[8])
+{
+    float g[8];
+    ld_weights8<TAIL>(a.w_post, a.w_bf16, 0, k, a.H, w);
+    ld_weights8<TAIL>(gate, a.w_bf16, row, k, a.H, g);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e] = a.beta * g[e] * w[e];
+}
+
 // A token held in registers: G threads, C chunks of 8 elements each, every
 // byte moved once.  The weights stay in registers over the tokens of a group
 // of threads, and so does the gate while its row lasts.
@@ -120,13 +136,14 @@ __global__ __launch_bounds__(row_block<G>()) void block_norm_kernel(const NormAr
     int64_t t = (int64_t)blockIdx.x * kRows + threadIdx.x / G;
     if constexpr (G == 64) t = __builtin_amdgcn_readfirstlane((int)t);
     const int64_t step = (int64_t)gridDim.x * kRows;
-    float w_post[C][8], w_pre[C][8], gate[C][8];
+    float w[C][8], w_pre[C][8];                              // w: beta gate w_post
+    auto weights = [&](const void* gate, int64_t row) {
 #pragma unroll
-    for (int j = 0; j < C; ++j) {
-        ld_weights8<TAIL>(a.w_post, a.w_bf16, 0, 8 * (g + G * j), a.H, w_post[j]);
-        ld_weights8<TAIL>(a.w_pre, a.w_bf16, 0, 8 * (g + G * j), a.H, w_pre[j]);
-        ld_weights8<TAIL>(nullptr, 0, 0, 0, 0, gate[j]);
-    }
+        for (int j = 0; j < C; ++j) ld_branch8<TAIL>(a, gate, row, 8 * (g + G * j), w[j]);
+    };
+    weights(nullptr, 0);
+#pragma unroll
+    for (int j = 0; j < C; ++j) ld_weights8<TAIL>(a.w_pre, a.w_bf16, 0, 8 * (g + G * j), a.H, w_pre[j]);
     uint32_t gate_row = ~0u;
     int turn = 0;
     for (; t < a.T; t += step) {
@@ -140,12 +157,8 @@ __global__ __launch_bounds__(row_block<G>()) void block_norm_kernel(const NormAr
         }
         if (a.gate) {
             const uint32_t row = (uint32_t)t / a.gate_tokens;
-            if (row != gate_row) {
-#pragma unroll
-                for (int j = 0; j < C; ++j)
-                    ld_weights8<TAIL>(a.gate, a.w_bf16, (int64_t)row * a.ld_gate, 8 * (g + G * j), a.H, gate[j]);
-                gate_row = row;
-            }
+            if (row != gate_row) weights(a.gate, (int64_t)row * a.ld_gate);
+            gate_row = row;
         }
         float kx = 1.0f;
         if (a.post) {
@@ -162,8 +175,7 @@ __global__ __launch_bounds__(row_block<G>()) void block_norm_kernel(const NormAr
         for (int j = 0; j < C; ++j) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float z = raw_get(x[j], e) * kx * w_post[j][e];
-                v[j][e] = a.rho * raw_get(r[j], e) + a.beta * (gate[j][e] * z);
+                v[j][e] = fmaf(raw_get(x[j], e) * kx, w[j][e], a.rho * raw_get(r[j], e));
                 s = fmaf(v[j][e], v[j][e], s);
             }
             if (a.r_out) st_row8<RB, TAIL>(a.r_out, t * a.ld_r_out, 8 * (g + G * j), a.H, v[j]);
@@ -309,7 +321,7 @@ __global__ __launch_bounds__(kBlock) void norm_bwd_weights_kernel(const NormBwdA
     const NormArgs& a = b.f;
     const int c = blockIdx.x * kBlock + threadIdx.x;
     if (c >= a.H) return;
-    const int64_t per = (a.T + b.chunks - 1) / b.chunks;
+    const int64_t per = (a.T + b.chunks - 1) / b.chunks;   // chunks > 0: there are tokens
     const int64_t t1 = min(a.T, (blockIdx.y + 1) * per);
     float post = 0.0f, pre = 0.0f;
     for (int64_t t = blockIdx.y * per; t < t1; ++t) {
@@ -336,12 +348,12 @@ __global__ __launch_bounds__(kBlock) void norm_bwd_weights_sum_kernel(const Norm
 }
 
 // a gate row's gradient: one column per thread, gate rows along blockIdx.y
-__global__ __launch_bounds__(kBlock) void norm_bwd_gate_kernel(const NormBwdArgs b, int64_t rows)
+__global__ __launch_bounds__(kBlock) void norm_bwd_gate_kernel(const NormBwdArgs b)
 {
     const NormArgs& a = b.f;
     const int c = blockIdx.x * kBlock + threadIdx.x;
     if (c >= a.H) return;
-    for (int64_t g = blockIdx.y; g < rows; g += gridDim.y) {
+    for (int64_t g = blockIdx.y; g < b.gate_rows; g += gridDim.y) {
         const int64_t t1 = min(a.T, (g + 1) * (int64_t)a.gate_tokens);
         float s = 0.0f;
         for (int64_t t = g * (int64_t)a.gate_tokens; t < t1; ++t) {
@@ -366,6 +378,274 @@ __global__ __launch_bounds__(kBlock) void norm_bwd_apply_kernel(const NormBwdArg
                 st_elem(b.dx, a.x_bf16, t * b.ld_dx + c,
                         a.post ? s.x * (g.dz * g.e.w_post - g.e.n_x * s.w) : g.dz);
         }
+    }
+}
+
+// Tokens held in registers, every row moved once.  A group of G threads takes
+// `per` consecutive tokens and keeps its columns' sums in registers over them;
+// the next token's rows are loaded before this one is worked on.
+//
+// Two sums for three gradients: with A = sum of d n_x over a gate row's tokens
+// (n_x = x without the post norm), dgate = beta w_post A, and dw_post is the
+// sum of beta gate A over the gate rows.
+//
+// Partial sums go to the workspace and norm_bwd_sum_kernel adds them in a
+// fixed order, so equal inputs give equal bits:
+//  * dw_post and dw_pre: the groups of a block meet in LDS, one partial a block;
+//  * dgate: a gate row that lies inside one group's tokens is written at
+//    once; one that a group shares with others goes to that group's slot 0
+//    (its first gate row) or 1 (its last).  A block whose tokens all share
+//    one gate row adds its groups up in LDS and uses its first slot only.
+// Three reductions a token: sum x^2; sum r'^2 with sum dh w_pre r'; and
+// sum dz w_post x.
+template <int G, int C, bool XB, bool RB, bool HB, bool TAIL>
+__global__ __launch_bounds__(row_block<G>()) void block_norm_bwd_kernel(const NormBwdArgs b)
+{
+    constexpr int kGroups = row_block<G>() / G;
+    __shared__ __align__(8) float red[G > 64 ? 6 * G / 64 : 2];
+    __shared__ float meet[kGroups > 1 ? (kGroups - 1) * G * C * 8 : 1];
+    const NormArgs& a = b.f;
+    const int g = threadIdx.x % G, q = threadIdx.x / G;
+    const int64_t group = (int64_t)blockIdx.x * kGroups + q;
+    uint32_t t0 = (uint32_t)min(a.T, group * b.per), t1 = (uint32_t)min(a.T, (group + 1) * b.per);
+    if constexpr (G == 64) {
+        t0 = __builtin_amdgcn_readfirstlane(t0);
+        t1 = __builtin_amdgcn_readfirstlane(t1);
+    }
+    // Where no gate row ends, neighbouring tokens go to neighbouring groups,
+    // so that the chip works on one stretch of memory at a time.
+    const uint32_t step = b.spread ? b.groups : 1;
+    if (b.spread) {
+        t0 = min((uint32_t)group, (uint32_t)a.T);
+        t1 = group < b.groups ? (uint32_t)a.T : t0;
+    }
+    const float invH = 1.0f / (float)a.H;
+    float s_post[C][8], s_pre[C][8], sum[C][8], w[C][8], w_pre[C][8];   // w: beta gate w_post
+    auto weights = [&](const void* gate, int64_t row) {
+#pragma unroll
+        for (int j = 0; j < C; ++j) ld_branch8<TAIL>(a, gate, row, 8 * (g + G * j), w[j]);
+    };
+    weights(nullptr, 0);
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+        ld_weights8<TAIL>(a.w_pre, a.w_bf16, 0, 8 * (g + G * j), a.H, w_pre[j]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s_post[j][e] = s_pre[j][e] = sum[j][e] = 0.0f;
+    }
+    // whole block on one gate row (its dgate is then left to the block's end)
+    const uint32_t bt0 = (uint32_t)min(a.T, (int64_t)blockIdx.x * kGroups * b.per);
+    const uint32_t bt1 = (uint32_t)min(a.T, ((int64_t)blockIdx.x + 1) * kGroups * b.per);
+    const bool one_row = a.gate && a.gate_tokens > 1 && bt1 > bt0 && bt0 / a.gate_tokens == (bt1 - 1) / a.gate_tokens;
+    // dw_post takes up the sum of a gate row (or of all tokens), the sum becomes dgate
+    auto close = [&](const void* gate, int64_t row) {
+#pragma unroll
+        for (int j = 0; j < C; ++j) {
+            float v[8];
+            ld_weights8<TAIL>(gate, a.w_bf16, row, 8 * (g + G * j), a.H, v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s_post[j][e] = fmaf(a.beta * v[e], sum[j][e], s_post[j][e]);
+            ld_weights8<TAIL>(a.w_post, a.w_bf16, 0, 8 * (g + G * j), a.H, v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum[j][e] *= a.beta * v[e];
+        }
+    };
+    auto put = [&](float* to, int64_t row, float (&v)[C][8]) {
+#pragma unroll
+        for (int j = 0; j < C; ++j) st_row8<false, TAIL>(to, row, 8 * (g + G * j), a.H, v[j]);
+    };
+    // the gate row that ends (for this group) at token `end`
+    auto flush = [&](uint32_t row, uint32_t end) {
+        close(a.gate, (int64_t)row * a.ld_gate);
+        if (b.dgate && !one_row) {
+            const uint64_t r0 = (uint64_t)row * a.gate_tokens;
+            const bool whole = r0 >= t0 && (r0 + a.gate_tokens <= end || end == (uint32_t)a.T);
+            if (whole) put(b.dgate, (int64_t)row * b.ld_dgate, sum);
+            else put(b.gpart, (2 * group + (r0 > t0 ? 1 : 0)) * (int64_t)a.H, sum);
+        }
+    };
+
+    Raw8<XB> x[C], nx[C];
+    Raw8<RB> r[C], nr[C], up[C], nup[C];
+    Raw8<HB> dh[C], ndh[C];
+    auto load = [&](uint32_t t) {
+#pragma unroll
+        for (int j = 0; j < C; ++j) {
+            const int k = 8 * (g + G * j);
+            nx[j] = ld_raw8<XB, TAIL>(a.x, (int64_t)t * a.ld_x, k, a.H);
+            nr[j] = ld_raw8<RB, TAIL>(a.r, (int64_t)t * a.ld_r, k, a.r ? a.H : 0);
+            ndh[j] = ld_raw8<HB, TAIL>(b.dh, (int64_t)t * b.ld_dh, k, b.dh ? a.H : 0);
+            nup[j] = ld_raw8<RB, TAIL>(b.dr_out, (int64_t)t * b.ld_dr_out, k, b.dr_out ? a.H : 0);
+        }
+    };
+    uint32_t gate_row = ~0u;
+    int turn = 0;
+    if (t0 < t1) load(t0);
+    for (uint32_t t = t0; t < t1; t += step) {
+#pragma unroll
+        for (int j = 0; j < C; ++j) { x[j] = nx[j]; r[j] = nr[j]; dh[j] = ndh[j]; up[j] = nup[j]; }
+        if (a.gate) {
+            const uint32_t row = t / a.gate_tokens;
+            if (row != gate_row) {
+                if (gate_row != ~0u) {
+                    flush(gate_row, t);
+#pragma unroll
+                    for (int j = 0; j < C; ++j)
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) sum[j][e] = 0.0f;
+                }
+                weights(a.gate, (int64_t)row * a.ld_gate);
+                gate_row = row;
+            }
+        }
+        if (t + step < t1) load(t + step);
+        float kx = 1.0f;
+        if (a.post) {
+            float s = 0.0f;
+#pragma unroll
+            for (int j = 0; j < C; ++j)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) s = fmaf(raw_get(x[j], e), raw_get(x[j], e), s);
+            kx = norm_factor(row_sum<G>(s, red, turn++), a.H, a.eps);
+        }
+        float v[C][8];                                       // r', then d
+        float s = 0.0f, p = 0.0f;
+#pragma unroll
+        for (int j = 0; j < C; ++j)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                v[j][e] = fmaf(raw_get(x[j], e) * kx, w[j][e], a.rho * raw_get(r[j], e));
+                s = fmaf(v[j][e], v[j][e], s);
+                p = fmaf(raw_get(dh[j], e) * w_pre[j][e], v[j][e], p);
+            }
+        row_sum2<G>(s, p, red + (G > 64 ? 2 * G / 64 : 0), turn);
+        ++turn;
+        const float kr = norm_factor(s, a.H, a.eps);
+        const float km = p * kr * invH * kr;                 // k_r mean(dh w_pre n_r)
+        float o = 0.0f;
+#pragma unroll
+        for (int j = 0; j < C; ++j)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float n = v[j][e] * kr, h = raw_get(dh[j], e), xe = raw_get(x[j], e);
+                s_pre[j][e] = fmaf(h, n, s_pre[j][e]);
+                v[j][e] = fmaf(-n, km, fmaf(kr, h * w_pre[j][e], raw_get(up[j], e)));
+                sum[j][e] = fmaf(v[j][e], xe * kx, sum[j][e]);
+                o = fmaf(v[j][e] * w[j][e], xe, o);
+            }
+        if (b.dr) {
+#pragma unroll
+            for (int j = 0; j < C; ++j) {
+                float y[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[e] = a.rho * v[j][e];
+                st_row8<RB, TAIL>(b.dr, (int64_t)t * b.ld_dr, 8 * (g + G * j), a.H, y);
+            }
+        }
+        if (b.dx) {
+            float mx = 0.0f;                                 // k_x^2 mean(dz w_post n_x)
+            if (a.post) mx = row_sum<G>(o, red, turn++) * kx * invH * kx * kx;
+#pragma unroll
+            for (int j = 0; j < C; ++j) {
+                float y[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[e] = fmaf(-raw_get(x[j], e), mx, kx * (v[j][e] * w[j][e]));
+                st_row8<XB, TAIL>(b.dx, (int64_t)t * b.ld_dx, 8 * (g + G * j), a.H, y);
+            }
+        }
+    }
+    if (!a.gate) close(nullptr, 0);
+    else if (gate_row != ~0u) flush(gate_row, t1);
+
+    // sums of the block: group 0 adds the others' from LDS
+    auto gather = [&](float (&v)[C][8]) {
+        if constexpr (kGroups > 1) {
+            if (q > 0) {
+#pragma unroll
+                for (int j = 0; j < C; ++j)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) meet[(((q - 1) * C + j) * 8 + e) * G + g] = v[j][e];
+            }
+            __syncthreads();
+            if (q == 0) {
+#pragma unroll
+                for (int j = 0; j < C; ++j)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        for (int o = 0; o < kGroups - 1; ++o) v[j][e] += meet[((o * C + j) * 8 + e) * G + g];
+            }
+            __syncthreads();
+        }
+    };
+    if (b.dgate && one_row) {
+        gather(sum);
+        if (q == 0) put(b.gpart, 2 * group * (int64_t)a.H, sum);
+    }
+    gather(s_post);
+    gather(s_pre);
+    if (q == 0) {
+        put(b.part, (int64_t)(2 * blockIdx.x) * a.H, s_post);
+        put(b.part, (int64_t)(2 * blockIdx.x + 1) * a.H, s_pre);
+    }
+}
+
+// Adds the partial sums: blockIdx.x a strip of 64 columns, blockIdx.y 0 and 1
+// dw_post and dw_pre, from 2 on the gate rows.  16 waves share a column's
+// partials and meet in LDS.
+constexpr int kSumWaves = 16;
+__global__ __launch_bounds__(64 * kSumWaves) void norm_bwd_sum_kernel(const NormBwdArgs b, int groups_of_block)
+{
+    __shared__ float meet[kSumWaves][64];
+    const NormArgs& a = b.f;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int c = blockIdx.x * 64 + lane;
+    auto finish = [&](float s, float* to) {
+        meet[wave][lane] = s;
+        __syncthreads();
+        if (wave == 0 && c < a.H) {
+#pragma unroll
+            for (int w = 1; w < kSumWaves; ++w) s += meet[w][lane];
+            *to = s;
+        }
+        __syncthreads();
+    };
+    if (blockIdx.y < 2) {
+        float* to = blockIdx.y ? b.dw_pre : b.dw_post;
+        if (!to) return;
+        float s = 0.0f;
+        if (c < a.H) {
+#pragma unroll 8
+            for (int k = wave; k < b.chunks; k += kSumWaves) s += b.part[(int64_t)(2 * k + blockIdx.y) * a.H + c];
+        }
+        finish(s, to + c);
+        return;
+    }
+    const uint32_t block_tokens = b.per * groups_of_block;
+    // A row that is not written yet ends its first group (or goes past it),
+    // so where there are more rows than groups it is found by the group.
+    const bool by_row = b.gate_rows <= b.groups;
+    const uint32_t n = by_row ? b.gate_rows : b.groups;
+    for (uint32_t i = blockIdx.y - 2; i < n; i += gridDim.y - 2) {
+        const uint32_t row = by_row ? i : ((uint32_t)min(a.T, (int64_t)(i + 1) * b.per) - 1) / a.gate_tokens;
+        const uint32_t r0 = row * a.gate_tokens, r1 = (uint32_t)min(a.T, (int64_t)r0 + a.gate_tokens);
+        const uint32_t q0 = r0 / b.per, q1 = (r1 - 1) / b.per;
+        if (!by_row && q0 != i) continue;
+        // inside one group, in a block with other gate rows: already written
+        const uint32_t blk = r0 / block_tokens;
+        const uint32_t b0 = blk * block_tokens, b1 = (uint32_t)min(a.T, (int64_t)b0 + block_tokens);
+        const bool shared_block = b0 / a.gate_tokens == (b1 - 1) / a.gate_tokens;
+        if (q0 == q1 && !shared_block) continue;
+        float s = 0.0f;
+        if (c < a.H) {
+#pragma unroll 4
+            for (uint32_t k = q0 + wave; k <= q1; k += kSumWaves) {
+                const uint32_t k0 = k / groups_of_block * block_tokens;
+                const uint32_t k1 = (uint32_t)min(a.T, (int64_t)k0 + block_tokens);
+                const bool one = k0 / a.gate_tokens == (k1 - 1) / a.gate_tokens;
+                if (one && k % groups_of_block) continue;    // added up in its block's first group
+                s += b.gpart[(int64_t)(2 * k + (r0 > k * b.per ? 1 : 0)) * a.H + c];
+            }
+        }
+        finish(s, b.dgate + (int64_t)row * b.ld_dgate + c);
     }
 }
 

@@ -141,6 +141,23 @@ __device__ __forceinline__ float row_sum(float v, float* red, int turn)
     }
     return v;
 }
+// two sums at once (`red`: two words per wave and turn)
+template <int G>
+__device__ __forceinline__ void row_sum2(float& v, float& w, float* red, int turn)
+{
+    v = wave_sum(v);
+    w = wave_sum(w);
+    if constexpr (G > 64) {
+        float* r = red + (turn & 1) * (2 * G / 64);
+        if ((threadIdx.x & 63u) == 0) *(f32x2*)(r + 2 * (threadIdx.x >> 6)) = f32x2{v, w};
+        __syncthreads();
+        f32x2 s = *(const f32x2*)r;
+#pragma unroll
+        for (int k = 1; k < G / 64; ++k) s += *(const f32x2*)(r + 2 * k);
+        v = s.x;
+        w = s.y;
+    }
+}
 template <int G>
 __device__ __forceinline__ uint32_t row_max_u32(uint32_t v, float* red, int turn)
 {
@@ -156,8 +173,9 @@ __device__ __forceinline__ uint32_t row_max_u32(uint32_t v, float* red, int turn
     return v;
 }
 
-// blocks of a row kernel: G threads a row, at least 256 a block
+// threads of a row kernel's block: four rows of a wave each, or one row (whose
+// reductions are barriers of the block)
 template <int G>
-constexpr int row_block() { return G < 256 ? 256 : G; }
+constexpr int row_block() { return G == 64 ? 256 : G; }
 
 }  // namespace echo

@@ -276,59 +276,68 @@ def echo_linear_int8(x, ldx, x_dtype, w, ldw, sw, bias, M, N, K, y, ldy, y_dtype
         workspace_bytes, _stream(stream)))
 
 
-def _rows(t, shape, what, dtypes):
-    """(pointer, row distance) of a matrix of contiguous rows; the C side cannot see a tensor's shape."""
-    if t.shape != shape or t.dtype not in dtypes or (shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{what}: {tuple(t.shape)} {t.dtype} strides {t.stride()}, expected {tuple(shape)} in rows "
-                         f"of contiguous elements of {' or '.join(str(d) for d in dtypes)}")
-    return t.data_ptr(), t.stride(0)
+_FLOATS = (F32, BF16)
 
 
-def _vector(t, n, what, dtype):
-    if t.shape != (n,) or t.dtype != dtype or not t.is_contiguous():
-        raise ValueError(f"{what}: {tuple(t.shape)} {t.dtype}, expected {n} contiguous elements of {dtype}")
+def _refuse(t, shape, what, kinds):
+    want = " or ".join(str(d) for d, k in _DTYPES.items() if k in kinds)
+    raise ValueError(f"{what}: {tuple(t.shape)} {t.dtype} strides {t.stride()}, expected {tuple(shape)} of {want} in "
+                     "rows of contiguous elements")
+
+
+def _rows(t, shape, what, kinds):
+    """(pointer, row distance, type) of a matrix of contiguous rows; the C side cannot see a tensor's shape."""
+    ld = t.stride()
+    kind = _DTYPES.get(t.dtype)
+    if t.shape != shape or kind not in kinds or (ld[1] != 1 and shape[1] > 1):
+        _refuse(t, shape, what, kinds)
+    return t.data_ptr(), ld[0], kind
+
+
+def _vector(t, n, what, kind):
+    if t.numel() != n or t.dim() != 1 or _DTYPES.get(t.dtype) != kind or not t.is_contiguous():
+        _refuse(t, (n,), what, (kind,))
     return t.data_ptr()
-
-
-_FLOATS = (torch.float32, torch.bfloat16)
-_FLOAT = (torch.float32,)
-_ANY_H = (torch.float32, torch.bfloat16, torch.int8)
 
 
 def make_norm_args(x, r=None, r_out=None, h=None, h_scale=None, post=True, w_post=None, w_pre=None, gate=None,
                    gate_tokens=0, res_scale=1.0, block_scale=1.0, eps=1e-5):
     """Fill an echo_norm_args from tensors: x, r, r_out and h are [T, H] in
-    contiguous rows, w_post and w_pre [H], gate [ceil(T / gate_tokens), H]."""
+    contiguous rows (an 8-bit h may be wider), w_post and w_pre [H], gate
+    [ceil(T / gate_tokens), H].  It can be kept and used again while the
+    tensors live."""
     shape = x.shape
     T, H = shape
-    a = NormArgs()
-    a.T, a.H = T, H
-    a.post, a.eps, a.res_scale, a.block_scale = 1 if post else 0, eps, res_scale, block_scale
-    a.x, a.ld_x = _rows(x, shape, "x", _FLOATS)
-    a.x_dtype = _DTYPES[x.dtype]
-    rd = r.dtype if r is not None else r_out.dtype if r_out is not None else x.dtype
-    a.r_dtype = _DTYPES.get(rd, -1)
+    px, ld_x, kx = _rows(x, shape, "x", _FLOATS)
+    pr = ld_r = po = ld_o = ph = ld_h = pg = ld_g = ps = 0
+    kr, kh = kx, F32
     if r is not None:
-        a.r, a.ld_r = _rows(r, shape, "r", _FLOATS)
-    if r_out is not None:
-        a.r_out, a.ld_r_out = _rows(r_out, shape, "r_out", (rd,))
+        pr, ld_r, kr = _rows(r, shape, "r", _FLOATS)
+        if r_out is not None:
+            po, ld_o, _ = _rows(r_out, shape, "r_out", (kr,))
+    elif r_out is not None:
+        po, ld_o, kr = _rows(r_out, shape, "r_out", _FLOATS)
     if h is not None:
-        a.h, a.ld_h = _rows(h[:, :H] if h.dtype == torch.int8 else h, shape, "h", _ANY_H)
-        a.h_dtype = _DTYPES[h.dtype]
-        if h.dtype == torch.int8 and h_scale is not None:
-            a.h_scale = _vector(h_scale, T, "h_scale", torch.float32)
-    wd = next((w.dtype for w in (w_post, w_pre, gate) if w is not None), torch.float32)
-    a.w_dtype = _DTYPES.get(wd, -1)
-    if w_post is not None:
-        a.w_post = _vector(w_post, H, "w_post", wd)
-    if w_pre is not None:
-        a.w_pre = _vector(w_pre, H, "w_pre", wd)
+        if h.dtype == torch.int8:
+            ph, ld_h, kh = _rows(h[:, :H], shape, "h", (I8,))
+            if h_scale is not None:
+                ps = _vector(h_scale, T, "h_scale", F32)
+        else:
+            ph, ld_h, kh = _rows(h, shape, "h", _FLOATS)
+    w = w_post if w_post is not None else w_pre if w_pre is not None else gate
+    kw = F32 if w is None else _DTYPES.get(w.dtype)
+    if kw not in _FLOATS:
+        raise ValueError(f"weights of {w.dtype}")
+    pp = _vector(w_post, H, "w_post", kw) if w_post is not None else 0
+    pw = _vector(w_pre, H, "w_pre", kw) if w_pre is not None else 0
     if gate is not None:
         if gate_tokens < 1:
             raise ValueError("a gate needs gate_tokens >= 1")
-        a.gate_tokens = gate_tokens
-        a.gate, a.ld_gate = _rows(gate, (-(-T // gate_tokens), H), "gate", (wd,))
-    return a
+        pg, ld_g, _ = _rows(gate, (-(-T // gate_tokens), H), "gate", (kw,))
+    else:
+        gate_tokens = 0
+    return NormArgs(T, H, ld_x, ld_r, ld_o, ld_h, ld_g, gate_tokens, kx, kr, kw, kh, 1 if post else 0, eps, res_scale,
+                    block_scale, px, pr, pp, pw, pg, po, ph, ps)
 
 
 def make_norm_grads(dh=None, dr_out=None, dx=None, dr=None, dw_post=None, dw_pre=None, dgate=None, workspace=None,
@@ -336,34 +345,28 @@ def make_norm_grads(dh=None, dr_out=None, dx=None, dr=None, dw_post=None, dw_pre
     """Fill an echo_norm_grads from tensors, shaped as in make_norm_args.
     Whether they fit its arguments (shape, types of dx, dr and dr_out, rows of
     dgate) is checked by echo_block_norm_backward."""
-    g = NormGrads()
-    g.shape = next((t.shape for t in (dh, dr_out, dx, dr) if t is not None), None)
-    g.types = set()
+    first = dh if dh is not None else dr_out if dr_out is not None else dx if dx is not None else dr
+    shape = None if first is None else first.shape
+    H = 0 if shape is None else shape[1]
+    ph = ld_h = pu = ld_u = px = ld_x = pr = ld_r = pg = ld_g = 0
+    kh, kx, ku, kr, rows = F32, None, None, None, None
     if dh is not None:
-        g.dh, g.ld_dh = _rows(dh, g.shape, "dh", _FLOATS)
-        g.dh_dtype = _DTYPES[dh.dtype]
+        ph, ld_h, kh = _rows(dh, shape, "dh", _FLOATS)
     if dr_out is not None:
-        g.dr_out, g.ld_dr_out = _rows(dr_out, g.shape, "dr_out", _FLOATS)
-        g.types.add(("r", _DTYPES[dr_out.dtype]))
-    if dr is not None:
-        g.dr, g.ld_dr = _rows(dr, g.shape, "dr", _FLOATS)
-        g.types.add(("r", _DTYPES[dr.dtype]))
+        pu, ld_u, ku = _rows(dr_out, shape, "dr_out", _FLOATS)
     if dx is not None:
-        g.dx, g.ld_dx = _rows(dx, g.shape, "dx", _FLOATS)
-        g.types.add(("x", _DTYPES[dx.dtype]))
-    H = g.shape[1] if g.shape is not None else 0
-    if dw_post is not None:
-        g.dw_post = _vector(dw_post, H, "dw_post", torch.float32)
-    if dw_pre is not None:
-        g.dw_pre = _vector(dw_pre, H, "dw_pre", torch.float32)
-    g.gate_rows = None
+        px, ld_x, kx = _rows(dx, shape, "dx", _FLOATS)
+    if dr is not None:
+        pr, ld_r, kr = _rows(dr, shape, "dr", _FLOATS)
+    pp = _vector(dw_post, H, "dw_post", F32) if dw_post is not None else 0
+    pw = _vector(dw_pre, H, "dw_pre", F32) if dw_pre is not None else 0
     if dgate is not None:
-        g.gate_rows = dgate.shape[0]
-        g.dgate, g.ld_dgate = _rows(dgate, (g.gate_rows, H), "dgate", _FLOAT)
-    g.workspace = _ptr(workspace)
+        rows = dgate.shape[0]
+        pg, ld_g, _ = _rows(dgate, (rows, H), "dgate", (F32,))
     if workspace_bytes is None:
         workspace_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    g.workspace_bytes = workspace_bytes
+    g = NormGrads(ld_h, ld_u, ld_x, ld_r, ld_g, kh, ph, pu, px, pr, pp, pw, pg, _ptr(workspace), workspace_bytes)
+    g.fits = (shape, kx, ku, kr, rows)
     return g
 
 
@@ -376,10 +379,10 @@ def echo_block_norm_backward_workspace_bytes(T, H) -> int:
 
 
 def echo_block_norm_backward(args: NormArgs, grads: NormGrads, stream=None):
-    if getattr(grads, "shape", None) is not None:
-        kinds = {"x": args.x_dtype, "r": args.r_dtype}
-        if (grads.shape != (args.T, args.H) or any(kinds[k] != d for k, d in grads.types)
-                or grads.gate_rows not in (None, -(-args.T // args.gate_tokens) if args.gate else 0)):
-            raise ValueError("the gradients' shapes or types do not fit the forward call's arguments")
+    shape, kx, ku, kr, rows = getattr(grads, "fits", (None,) * 5)      # set by make_norm_grads
+    if ((shape is not None and shape != (args.T, args.H)) or kx not in (None, args.x_dtype)
+            or ku not in (None, args.r_dtype) or kr not in (None, args.r_dtype)
+            or (rows is not None and rows != (-(-args.T // args.gate_tokens) if args.gate else 0))):
+        raise ValueError("the gradients' shapes or types do not fit the forward call's arguments")
     _check("echo_block_norm_backward", _lib.echo_block_norm_backward(
         ctypes.byref(args), ctypes.byref(grads), _stream(stream)))
