@@ -86,9 +86,13 @@ void gemm_few_go(const echo::GemmI8Args& a, const void* xf, hipStream_t st)
     f.g = a;
     f.xf = xf;
     f.pitch = echo::few_pitch(a.K);
+    // every row of codes starts on a word
+    const bool words = aligned_to(a.w, 4) && a.ldw % 4 == 0 && (XKIND || (aligned_to(a.x, 4) && a.ldx % 4 == 0));
     const size_t parts = (size_t)echo::kFewWaves * MT * 1024, codes = XKIND ? (size_t)a.M * f.pitch : 0;
-    hipLaunchKernelGGL((echo::gemm_i8_few_kernel<MT, XKIND, FM, C>), dim3((unsigned)((a.N + 15) / 16)),
-                       dim3(echo::kFewThreads), parts > codes ? parts : codes, st, f);
+    const size_t lds = parts > codes ? parts : codes;
+    const dim3 grid((unsigned)((a.N + 15) / 16)), block(echo::kFewThreads);
+    if (words) hipLaunchKernelGGL((echo::gemm_i8_few_kernel<MT, XKIND, FM, C, false>), grid, block, lds, st, f);
+    else hipLaunchKernelGGL((echo::gemm_i8_few_kernel<MT, XKIND, FM, C, true>), grid, block, lds, st, f);
 }
 
 // Layers that one launch quantizes and multiplies, while the tokens fit the
@@ -108,13 +112,14 @@ void linear_fused_go(const echo::GemmI8Args& a, const void* x, hipStream_t st)
     else one ? gemm_few_go<1, XKIND, 4, 1>(a, x, st) : gemm_few_go<1, XKIND, 4, 2>(a, x, st);
 }
 
-// Tiles: one of the five sizes, by the estimated time of all rounds of tiles
+// Tiles: one of the sizes below, by the estimated time of all rounds of tiles
 // over the CUs.  `us` is a full chip's round of that tile at K = 4096 as
 // measured, with direct loads and through registers; all grow alike with K.
 // The largest tile reads the least per product and wins where it fills the
 // chip (16384 x 4096 x 4096: 238 us, 270 with 128 x 256, 550 with 64 x 64);
-// small calls want a tile for every CU (100 x 4096 x 4096: 38 us with 256 x
-// 256, 9.6 with 64 x 64).  Through registers the largest tile spills and
+// small calls want a tile for every CU, whose loads come at about 30 bytes a
+// clock whatever the tile (100 x 4096 x 4096: 38 us with 256 x 256, 9.7 with
+// 64 x 64, 8.9 with 64 x 32).  Through registers the largest tile spills and
 // gains nothing over the next one (88 us each at 4096 x 4096 x 3584).
 struct TileCost {
     int bm, bn;
@@ -124,15 +129,18 @@ constexpr TileCost kTiles[] = {{256, 256, {61.0f, 0.0f}},
                                {128, 256, {37.0f, 51.0f}},
                                {128, 128, {24.0f, 31.5f}},
                                {64, 128, {14.9f, 25.0f}},
-                               {64, 64, {9.6f, 15.8f}}};
+                               {64, 64, {9.7f, 16.6f}},
+                               {64, 32, {8.9f, 16.1f}}};
 constexpr int64_t kCus = 256;
 
 void launch_gemm_i8(echo::GemmI8Args& a, hipStream_t st)
 {
-    // Up to 32 tokens: the weight streams past the tokens, no tiles (27 x 4096
-    // x 3584: 8.2 us, 8.8 in 64 x 64 tiles; 16 x 1000 x 8192: 9.8 and 14.7;
-    // from 33 on the tiles win: 48 x 4096 x 4096: 12.2 and 9.6).
-    if (a.M <= 32 && grid_fits((a.N + 15) / 16, echo::kFewThreads)) {
+    // Few tokens: the weight streams past them, without tiles, while the blocks
+    // of 16 channels are about as many as the CUs: 16 x 4096 x 4096 in 7.5 us
+    // (9.6 in 64 x 64 tiles), 32 in 9.4 (9.8); each block reads the tokens
+    // again, so past that only up to 8 of them (16 x 8192 x 8192: 18.4 and
+    // 15.5, 8 tokens 15.4 and 15.5).
+    if ((a.M <= 8 || (a.M <= 32 && a.N <= 16 * kCus)) && grid_fits((a.N + 15) / 16, echo::kFewThreads)) {
         if (a.M <= 16) gemm_few_go<1, 0, 1, 1>(a, nullptr, st);
         else gemm_few_go<2, 0, 1, 1>(a, nullptr, st);
         return;
@@ -140,7 +148,7 @@ void launch_gemm_i8(echo::GemmI8Args& a, hipStream_t st)
     const bool direct = aligned16(a.x) && aligned16(a.w) && a.ldx % 16 == 0 && a.ldw % 16 == 0;
     int best = -1;
     float least = 0.0f;
-    for (int i = 0; i < 5; ++i) {
+    for (int i = 0; i < (int)(sizeof(kTiles) / sizeof(kTiles[0])); ++i) {
         const int64_t tiles = ((a.M + kTiles[i].bm - 1) / kTiles[i].bm) * ((a.N + kTiles[i].bn - 1) / kTiles[i].bn);
         const float t = (float)((tiles + kCus - 1) / kCus) * kTiles[i].us[direct ? 0 : 1];
         if (t > 0.0f && grid_fits(tiles, 512) && (best < 0 || t < least)) {
@@ -155,6 +163,7 @@ void launch_gemm_i8(echo::GemmI8Args& a, hipStream_t st)
     case 2: return gemm_stage_go<128, 128, 2, 4, 4, 2>(a, direct, st);
     case 3: return gemm_stage_go<64, 128, 2, 2, 4, 2>(a, direct, st);
     case 4: return gemm_stage_go<64, 64, 2, 2, 4, 4>(a, direct, st);
+    case 5: return gemm_stage_go<64, 32, 2, 1, 4, 2>(a, direct, st);
     default: break;
     }
     // rows too far apart for 32-bit offsets, or more tiles than a launch holds

@@ -251,6 +251,18 @@ __device__ __forceinline__ uint32_t i8_key(uint32_t r) { return (r & 7u) ^ ((r >
 // s_waitcnt operand: at most `left` vector-memory operations outstanding
 constexpr int waitcnt_vm(int left) { return 0x0F70 | (left & 15) | ((left >> 4) << 14); }
 
+// A barrier of the block that leaves `LEFT` vector-memory operations of each
+// wave on their way (and no LDS operation).  __syncthreads() would wait for
+// all of them, and so for the stages that are meant to be under way.
+template <int LEFT>
+__device__ __forceinline__ void stage_barrier()
+{
+    __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");   // for the compiler: no access moves across
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm(LEFT) & 0xF0FF);
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+}
+
 template <int BM, int BN, int WM, int WN, int NS, int NR>
 __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(WM * WN / 4, WM * WN / 4)))
 void gemm_i8_stage_kernel(const GemmI8Args a)
@@ -376,13 +388,13 @@ void gemm_i8_stage_kernel(const GemmI8Args a)
         }
     };
 
-    const int KT = a.K / kI8BK;
-    if (KT > 0) {
+    const int n = a.K / kI8BK;
+    if (n > 0) {
         if constexpr (DIRECT) {
-            for (int i = 0; i < NS && i < KT; ++i) issue(i, (uint32_t)i * kI8BK);
+            for (int i = 0; i < NS && i < n; ++i) issue(i, (uint32_t)i * kI8BK);
             // the first stage has landed when only the later ones' loads are out
-            if (KT >= NS) __builtin_amdgcn_s_waitcnt(waitcnt_vm((NS - 1) * (LM + LN)));
-            else __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+            if (n >= NS) stage_barrier<(NS - 1) * (LM + LN)>();
+            else stage_barrier<0>();
         } else {                                             // stage s waits in set s % NR
 #pragma unroll
             for (int i = 0; i < LM + LN; ++i) hold1(0, i, 0);
@@ -390,12 +402,12 @@ void gemm_i8_stage_kernel(const GemmI8Args a)
             for (int i = 0; i < LM + LN; ++i) put1(0, i, 0);
 #pragma unroll
             for (int s = 1; s <= NR; ++s)
-                if (s < KT) {
+                if (s < n) {
 #pragma unroll
                     for (int i = 0; i < LM + LN; ++i) hold1(s % NR, i, (uint32_t)s * kI8BK);
                 }
+            stage_barrier<63>();
         }
-        __syncthreads();
 #pragma unroll
         for (int f = 0; f < TM + TN; ++f) read1(0, f, place(0, 0));
         uint32_t buf = 0;
@@ -409,13 +421,12 @@ void gemm_i8_stage_kernel(const GemmI8Args a)
                 step(1, true, buf, 2, kNone, 0, 0, 0);
                 step(0, true, buf, 3, kNone, 0, 0, 0);
                 // this stage's fragments are in registers, the next stage has landed
-                __builtin_amdgcn_s_waitcnt(waitcnt_vm(decltype(left)::value * (LM + LN)) & 0xF0FF);
-                __syncthreads();
+                stage_barrier<decltype(left)::value * (LM + LN)>();
                 step(1, more, next, 0, loads ? kLoad : kNone, buf, k0, 0);
                 buf = next;
             };
-            for (; kt + NS < KT; ++kt) stage(std::integral_constant<int, NS - 2>{}, true, true, (uint32_t)(kt + NS) * kI8BK);
-            for (; kt + 1 < KT; ++kt) stage(std::integral_constant<int, 0>{}, true, false, 0);
+            for (; kt + NS < n; ++kt) stage(std::integral_constant<int, NS - 2>{}, true, true, (uint32_t)(kt + NS) * kI8BK);
+            for (; kt + 1 < n; ++kt) stage(std::integral_constant<int, 0>{}, true, false, 0);
             stage(std::integral_constant<int, 0>{}, false, false, 0);
         } else {
             // the next stage moves from its set to LDS, the set takes the
@@ -424,23 +435,23 @@ void gemm_i8_stage_kernel(const GemmI8Args a)
                 step(0, true, buf, 1, more ? kPut : kNone, buf ^ 1u, 0, rset);
                 step(1, true, buf, 2, loads ? kLoad : kNone, 0, (uint32_t)(at + 1 + NR) * kI8BK, rset);
                 step(0, true, buf, 3, kNone, 0, 0, 0);
-                __syncthreads();
+                stage_barrier<63>();
                 step(1, more, buf ^ 1u, 0, kNone, 0, 0, 0);
                 buf ^= 1u;
             };
-            for (; kt + 2 * NR < KT; kt += NR) {
+            for (; kt + 2 * NR < n; kt += NR) {
 #pragma unroll
                 for (int r = 0; r < NR; ++r) stage((r + 1) % NR, true, true, kt + r);
             }
-            for (; kt < KT; kt += NR) {
+            for (; kt < n; kt += NR) {
 #pragma unroll
                 for (int r = 0; r < NR; ++r)
-                    if (kt + r < KT) stage((r + 1) % NR, kt + r + 1 < KT, kt + r + 1 + NR < KT, kt + r);
+                    if (kt + r < n) stage((r + 1) % NR, kt + r + 1 < n, kt + r + 1 + NR < n, kt + r);
             }
         }
     }
     // what is left of K, through registers: bytes past K are zeros
-    if (KT * kI8BK < a.K) {
+    if (n * kI8BK < a.K) {
         __syncthreads();
         for (uint32_t i = tid; i < (BM + BN) * 8; i += NT) {
             const uint32_t r = i >> 3, c = i & 7u;
@@ -448,7 +459,7 @@ void gemm_i8_stage_kernel(const GemmI8Args a)
             const uint32_t q = isx ? r : r - BM;
             i32x4 v = {0, 0, 0, 0};
             if ((int)q < (isx ? rows_m : rows_n))
-                v = ld_codes16((isx ? px + (size_t)q * ldx : pw + (size_t)q * ldw), KT * kI8BK + 16 * (int)c, a.K);
+                v = ld_codes16((isx ? px + (size_t)q * ldx : pw + (size_t)q * ldw), n * kI8BK + 16 * (int)c, a.K);
             *(i32x4*)(smem + r * kI8BK + ((c ^ i8_key(q)) * 16u)) = v;
         }
         __syncthreads();
@@ -543,7 +554,35 @@ struct FewArgs {
 // whole steps of 64 codes, and 16 bytes that shift the tokens' banks
 constexpr int few_pitch(int K) { return (K + 63) / 64 * 64 + 16; }
 
-template <int MT, int XKIND, int FM, int C>
+// 16 codes on their way to registers.  SHIFT: the row may start between two
+// words; the words that hold the codes are loaded and shifted together (as
+// 16-byte loads at odd addresses: 14.4 us at 8 x 4096 x 4096, 6.7 aligned).
+template <bool SHIFT>
+struct Codes16 {
+    u32x4 v;
+    uint32_t last[1];
+    __device__ __forceinline__ void load(const int8_t* p)
+    {
+        if constexpr (SHIFT) {
+            const uint32_t t = (uint32_t)(uintptr_t)p & 3u;
+            __builtin_memcpy(&v, __builtin_assume_aligned(p - t, 4), 16);
+            // the fifth word holds none of the codes where they start on a word: the fourth again
+            __builtin_memcpy(last, __builtin_assume_aligned(p - t + (t ? 16 : 12), 4), 4);
+        } else {
+            __builtin_memcpy(&v, __builtin_assume_aligned(p, 4), 16);
+        }
+    }
+    __device__ __forceinline__ i32x4 get(uint32_t t) const   // t: the address, or its two low bits
+    {
+        if constexpr (SHIFT)
+            return i32x4{(int)__builtin_amdgcn_alignbyte(v.y, v.x, t), (int)__builtin_amdgcn_alignbyte(v.z, v.y, t),
+                         (int)__builtin_amdgcn_alignbyte(v.w, v.z, t), (int)__builtin_amdgcn_alignbyte(last[0], v.w, t)};
+        else
+            return i32x4{(int)v.x, (int)v.y, (int)v.z, (int)v.w};
+    }
+};
+
+template <int MT, int XKIND, int FM, int C, bool SHIFT>
 __global__ __launch_bounds__(kFewThreads) void gemm_i8_few_kernel(const FewArgs a)
 {
     extern __shared__ __align__(16) uint8_t few_lds[];
@@ -569,11 +608,12 @@ __global__ __launch_bounds__(kFewThreads) void gemm_i8_few_kernel(const FewArgs 
             for (int j = 0; j < C; ++j)
                 raw[m][j] = ld_raw8<XKIND == 1, true>(a.xf, m * g.ldx, 8 * ((int)tid + kFewThreads * j), m < M ? g.K : 0);
     }
-    i32x4 fw[kFewDepth];
+    Codes16<SHIFT> fw[kFewDepth];
+    const uint32_t tw = (uint32_t)(uintptr_t)wr;             // steps of 64 keep a row's place in its words
     auto load_w = [&](int s) {
 #pragma unroll
         for (int i = 0; i < kFewDepth; ++i)
-            if (s + i < full) __builtin_memcpy(&fw[i], wr + (int64_t)(s + i) * 64, 16);
+            if (s + i < full) fw[i].load(wr + (int64_t)(s + i) * 64);
     };
     load_w(s0);
 
@@ -613,31 +653,55 @@ __global__ __launch_bounds__(kFewThreads) void gemm_i8_few_kernel(const FewArgs 
     i32x4 acc[MT];
 #pragma unroll
     for (int t = 0; t < MT; ++t) acc[t] = i32x4{0, 0, 0, 0};
-    auto x_frag = [&](int t, int s) -> i32x4 {
-        const int m = 16 * t + (int)row;
-        i32x4 v = {0, 0, 0, 0};
-        if (m < M) {
-            if constexpr (XKIND > 0) v = *(const i32x4*)(few_lds + m * a.pitch + s * 64 + chunk);
-            else if (s < full) __builtin_memcpy(&v, g.x + m * g.ldx + (int64_t)s * 64 + chunk, 16);
-            else v = ld_codes16(g.x + m * g.ldx, s * 64 + (int)chunk, g.K);
-        }
-        return v;
+    // A lane past the last token repeats it: its sums are not stored, and a
+    // load without a condition can be on its way with all the others.
+    const int8_t* xr[MT];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+        const int m = min(16 * t + (int)row, M - 1);
+        xr[t] = XKIND > 0 ? (const int8_t*)few_lds + m * a.pitch : g.x + m * g.ldx;
+    }
+    constexpr bool XSHIFT = SHIFT && XKIND == 0;
+    auto x_load = [&](Codes16<XSHIFT>& f, int t, int s) {
+        if constexpr (XKIND > 0) f.v = *(const u32x4*)(xr[t] + s * 64 + chunk);
+        else f.load(xr[t] + (int64_t)s * 64 + chunk);
     };
-    for (int s = s0; s < full; s += kFewDepth) {
+    auto x_place = [&](int t) { return (uint32_t)(uintptr_t)xr[t]; };
+    int s = s0;
+    for (; s + kFewDepth <= full; s += kFewDepth) {
+        Codes16<XSHIFT> fx[MT][kFewDepth];
+#pragma unroll
+        for (int i = 0; i < kFewDepth; ++i)
+#pragma unroll
+            for (int t = 0; t < MT; ++t) x_load(fx[t][i], t, s + i);
 #pragma unroll
         for (int i = 0; i < kFewDepth; ++i) {
-            if (s + i < full) {
+            const i32x4 w = fw[i].get(tw);
 #pragma unroll
-                for (int t = 0; t < MT; ++t)
-                    acc[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[i], x_frag(t, s + i), acc[t], 0, 0, 0);
-            }
+            for (int t = 0; t < MT; ++t)
+                acc[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w, fx[t][i].get(x_place(t)), acc[t], 0, 0, 0);
         }
         load_w(s + kFewDepth);
+    }
+#pragma unroll
+    for (int i = 0; i < kFewDepth; ++i) {
+        if (s + i < full) {
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+                Codes16<XSHIFT> f;
+                x_load(f, t, s + i);
+                acc[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[i].get(tw), f.get(x_place(t)), acc[t], 0, 0, 0);
+            }
+        }
     }
     if (full < s1) {                                         // the step that K ends in
         const i32x4 w = ld_codes16(wr - chunk, full * 64 + (int)chunk, g.K);
 #pragma unroll
-        for (int t = 0; t < MT; ++t) acc[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w, x_frag(t, full), acc[t], 0, 0, 0);
+        for (int t = 0; t < MT; ++t) {
+            const i32x4 v = XKIND > 0 ? *(const i32x4*)(xr[t] + full * 64 + chunk)
+                                      : ld_codes16(xr[t], full * 64 + (int)chunk, g.K);
+            acc[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w, v, acc[t], 0, 0, 0);
+        }
     }
 
     // sum over the waves: lane l of tile t holds channels 4 (l / 16) .. + 3 of token 16 t + l % 16
