@@ -148,12 +148,16 @@ def _ptr(t):
 # torch's handle of a device's current stream; building a torch.cuda.Stream
 # for it costs 2.7 us, a third of a small call
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_gpu_seen = False
 
 
 def _stream(s):
     if s is None:
-        if not torch.cuda.is_available():
-            return None
+        global _gpu_seen
+        if not _gpu_seen:
+            if not torch.cuda.is_available():
+                return None
+            _gpu_seen = True
         if _raw_stream is not None:
             return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
@@ -319,7 +323,10 @@ def make_norm_args(x, r=None, r_out=None, h=None, h_scale=None, post=True, w_pos
         po, ld_o, kr = _rows(r_out, shape, "r_out", _FLOATS)
     if h is not None:
         if h.dtype == torch.int8:
-            ph, ld_h, kh = _rows(h[:, :H], shape, "h", (I8,))
+            n, wide = h.shape
+            if wide < H:
+                _refuse(h, shape, "h", (I8,))
+            ph, ld_h, kh = _rows(h, (n, wide) if n == T else shape, "h", (I8,))
             if h_scale is not None:
                 ps = _vector(h_scale, T, "h_scale", F32)
         else:

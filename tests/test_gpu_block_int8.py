@@ -179,6 +179,26 @@ def test_gemm_int8_workload_shapes(echo, M, N, K):
         same_bits(y, want.to(dt))
 
 
+@pytest.mark.parametrize("M,N", [(4096, 4096), (2048, 4096), (1024, 4096), (512, 4096), (200, 4100), (100, 4096), (40, 8200)])
+@pytest.mark.parametrize("K", [128, 300, 1155])
+@pytest.mark.parametrize("pad", [0, 1, 4])
+def test_gemm_int8_every_tile(echo, M, N, K, pad):
+    """Sizes that fill the chip with each tile, with rows at multiples of 16
+    bytes (pad 0), at words and at odd places; whole stages and a rest of K."""
+    say("gemm tiles", M, N, K, pad)
+    g = torch.Generator(device=DEV).manual_seed(M + N + K)
+    ld = -(-K // 16) * 16 + pad
+    x = torch.randint(-128, 128, (M, ld), generator=g, device=DEV, dtype=torch.int8)[:, :K]
+    w = torch.randint(-128, 128, (N, ld), generator=g, device=DEV, dtype=torch.int8)[:, :K]
+    sx, sw, b = torch.rand(M, generator=g, device=DEV), torch.rand(N, generator=g, device=DEV), torch.rand(N, generator=g, device=DEV)
+    want = ((x.double() @ w.double().t().contiguous()).float() * sx[:, None]) * sw + b
+    y = torch.full((M, N + pad), 7.0, dtype=torch.bfloat16, device=DEV)
+    echo.echo_gemm_int8(x, ld, sx, w, ld, sw, b, M, N, K, y, N + pad, echo.BF16)
+    torch.cuda.synchronize()
+    same_bits(y[:, :N].contiguous(), want.bfloat16())
+    assert bool((y[:, N:] == 7).all())
+
+
 @pytest.mark.parametrize("M", [1, 40, 300])
 def test_gemm_int8_far_rows(echo, M):
     """Row distances that put operands and outputs past 2^31 elements."""
