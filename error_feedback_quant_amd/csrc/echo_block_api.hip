@@ -244,7 +244,7 @@ bool with_bwd_shape(int64_t H, F f)
 struct BwdPlan {
     int64_t blocks;          // of the row kernel; chunks of tokens for long rows
     int64_t per, groups;     // tokens of a group, groups that have any
-    int group_size;          // groups of a block
+    int group_shift;         // a block has 1 << group_shift groups
     size_t stats, part, gpart, total;
 };
 constexpr int64_t kBwdWaves = 8;
@@ -262,17 +262,17 @@ BwdPlan bwd_plan(int64_t T, int64_t H)
     int threads = 0;
     with_bwd_shape(H, [&](auto g, auto) {
         threads = echo::row_block<decltype(g)::value>();
-        p.group_size = threads / decltype(g)::value;
+        for (p.group_shift = 0; (decltype(g)::value << p.group_shift) < threads; ++p.group_shift) {}
     });
     // two tokens a group at least, and 8 waves on a CU (more do not fit the
     // registers: 12 took 320 us at 131072 x 1024, 8 take 302) or one block
     int64_t most = kBwdWaves * 64 * kCus / threads;
     if (most < kCus) most = kCus;
-    most *= p.group_size;
+    most <<= p.group_shift;
     const int64_t groups = (T + 1) / 2 < most ? (T + 1) / 2 : most;
     p.per = groups ? (T + groups - 1) / groups : 1;
     p.groups = (T + p.per - 1) / p.per;
-    p.blocks = (p.groups + p.group_size - 1) / p.group_size;
+    p.blocks = (p.groups + (1 << p.group_shift) - 1) >> p.group_shift;
     p.gpart = align256((size_t)(p.blocks * 2 * H * 4));
     p.total = p.gpart + (size_t)(p.groups * 2 * H * 4);
     return p;
@@ -385,7 +385,7 @@ int launch_block_norm_bwd(const echo::NormBwdArgs& b, const BwdPlan& plan, hipSt
     if (rows > 4096) rows = 4096;
     if (!b.dw_post && !b.dw_pre && !rows) return ECHO_OK;
     hipLaunchKernelGGL(echo::norm_bwd_sum_kernel, dim3((unsigned)((a.H + 63) / 64), (unsigned)(2 + rows)),
-                       dim3(64 * echo::kSumWaves), 0, st, b, plan.group_size);
+                       dim3(64 * echo::kSumWaves), 0, st, b, plan.group_shift);
     return check_launch();
 }
 

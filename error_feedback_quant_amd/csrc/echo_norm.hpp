@@ -592,7 +592,7 @@ __global__ __launch_bounds__(row_block<G>()) void block_norm_bwd_kernel(const No
 // dw_post and dw_pre, from 2 on the gate rows.  16 waves share a column's
 // partials and meet in LDS.
 constexpr int kSumWaves = 16;
-__global__ __launch_bounds__(64 * kSumWaves) void norm_bwd_sum_kernel(const NormBwdArgs b, int groups_of_block)
+__global__ __launch_bounds__(64 * kSumWaves) void norm_bwd_sum_kernel(const NormBwdArgs b, int group_shift)
 {
     __shared__ float meet[kSumWaves][64];
     const NormArgs& a = b.f;
@@ -619,7 +619,7 @@ __global__ __launch_bounds__(64 * kSumWaves) void norm_bwd_sum_kernel(const Norm
         finish(s, to + c);
         return;
     }
-    const uint32_t block_tokens = b.per * groups_of_block;
+    const uint32_t block_tokens = b.per << group_shift;      // 1 << group_shift groups a block
     // A row that is not written yet ends its first group (or goes past it),
     // so where there are more rows than groups it is found by the group.
     const bool by_row = b.gate_rows <= b.groups;
@@ -629,20 +629,19 @@ __global__ __launch_bounds__(64 * kSumWaves) void norm_bwd_sum_kernel(const Norm
         const uint32_t r0 = row * a.gate_tokens, r1 = (uint32_t)min(a.T, (int64_t)r0 + a.gate_tokens);
         const uint32_t q0 = r0 / b.per, q1 = (r1 - 1) / b.per;
         if (!by_row && q0 != i) continue;
+        // a block that lies in the row has added up its groups (no division: they took half of this kernel's time)
+        auto inside = [&](uint32_t block) {
+            const uint32_t k0 = block * block_tokens;
+            return k0 >= r0 && (uint32_t)min(a.T, (int64_t)k0 + block_tokens) <= r1;
+        };
         // inside one group, in a block with other gate rows: already written
-        const uint32_t blk = r0 / block_tokens;
-        const uint32_t b0 = blk * block_tokens, b1 = (uint32_t)min(a.T, (int64_t)b0 + block_tokens);
-        const bool shared_block = b0 / a.gate_tokens == (b1 - 1) / a.gate_tokens;
-        if (q0 == q1 && !shared_block) continue;
+        if (q0 == q1 && !inside(q0 >> group_shift)) continue;
         float s = 0.0f;
         if (c < a.H) {
-#pragma unroll 4
+#pragma unroll 8
             for (uint32_t k = q0 + wave; k <= q1; k += kSumWaves) {
-                const uint32_t k0 = k / groups_of_block * block_tokens;
-                const uint32_t k1 = (uint32_t)min(a.T, (int64_t)k0 + block_tokens);
-                const bool one = k0 / a.gate_tokens == (k1 - 1) / a.gate_tokens;
-                if (one && k % groups_of_block) continue;    // added up in its block's first group
-                s += b.gpart[(int64_t)(2 * k + (r0 > k * b.per ? 1 : 0)) * a.H + c];
+                const bool added = ((k >> group_shift) << group_shift) != k && inside(k >> group_shift);
+                if (!added) s += b.gpart[(int64_t)(2 * k + (r0 > k * b.per ? 1 : 0)) * a.H + c];
             }
         }
         finish(s, b.dgate + (int64_t)row * b.ld_dgate + c);
