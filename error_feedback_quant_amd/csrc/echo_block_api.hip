@@ -130,7 +130,7 @@ constexpr TileCost kTiles[] = {{256, 256, {61.0f, 0.0f}},
                                {128, 128, {24.0f, 31.5f}},
                                {64, 128, {14.9f, 25.0f}},
                                {64, 64, {9.7f, 16.6f}},
-                               {64, 32, {8.9f, 16.1f}}};
+                               {64, 32, {8.9f, 14.6f}}};
 constexpr int64_t kCus = 256;
 
 void launch_gemm_i8(echo::GemmI8Args& a, hipStream_t st)

@@ -215,15 +215,16 @@ __global__ __launch_bounds__(kBlock) void gemm_i8_tile_kernel(const GemmI8Args a
 // the first fragments of the next stage are read under them; a barrier at the
 // stage's end would leave the matrix cores idle for an LDS round trip.
 //
-// Measured (direct loads): 4096 x 4096 x 3584 in 57 us (2.1 POP/s), 16384 x
-// 4096 x 4096 in 238 us (2.31 POP/s).  With 256 x 256 tiles the matrix cores
-// are busy for 61 % of a tile's cycles; a full chip then runs at about 1.8 GHz
-// (a quarter-full one at 2.4), so beyond that power bounds it: the 4-wave form
-// of the tile, with a third less LDS traffic but one wave on each SIMD, took
-// 62 us, and a 2 x 4 tile of 32 x 32 fragments for each wave reads 6 operands
-// for 8 MFMAs.  Small tiles are bound by the latency of their stages, hence
-// their deeper queues (64 x 64 at 777 x 1001 x 3584: 22 us with two stages in
-// registers at most, 11.4 with four on their way).
+// Measured (direct loads): 4096 x 4096 x 3584 in 55 us (2.19 POP/s), 16384 x
+// 4096 x 4096 in 248 us (2.22 POP/s).  With 256 x 256 tiles the matrix cores
+// are busy for 64 % of a tile's cycles; a full chip then runs at about 1.8 GHz
+// (half of it at 2.4: 63 us for 256 tiles of K = 4096, 46 for 128), so beyond
+// that power bounds it: the 4-wave form of the tile, with a third less LDS
+// traffic but one wave on each SIMD, took 62 us.  Small tiles are bound by
+// their loads, which come at about 30 bytes a clock and CU whatever the tile;
+// splitting K over two halves of a block, or reading a whole stage's
+// fragments at once, made them no faster.  Rows at odd places need a fifth
+// word for each 16 bytes and more lines: 88 us at 4096 x 4096 x 3584.
 
 constexpr int kI8BK = 128;                   // bytes of K per stage
 constexpr int64_t kI8StageLd = int64_t(1) << 22;   // row distances below this keep a panel's offsets in 31 bits
@@ -390,29 +391,18 @@ void gemm_i8_stage_kernel(const GemmI8Args a)
 
     const int n = a.K / kI8BK;
     if (n > 0) {
+        uint32_t buf = 0;
+        int kt = 0;
+        auto read_first = [&] {
+#pragma unroll
+            for (int f = 0; f < TM + TN; ++f) read1(0, f, place(0, 0));
+        };
         if constexpr (DIRECT) {
             for (int i = 0; i < NS && i < n; ++i) issue(i, (uint32_t)i * kI8BK);
             // the first stage has landed when only the later ones' loads are out
             if (n >= NS) stage_barrier<(NS - 1) * (LM + LN)>();
             else stage_barrier<0>();
-        } else {                                             // stage s waits in set s % NR
-#pragma unroll
-            for (int i = 0; i < LM + LN; ++i) hold1(0, i, 0);
-#pragma unroll
-            for (int i = 0; i < LM + LN; ++i) put1(0, i, 0);
-#pragma unroll
-            for (int s = 1; s <= NR; ++s)
-                if (s < n) {
-#pragma unroll
-                    for (int i = 0; i < LM + LN; ++i) hold1(s % NR, i, (uint32_t)s * kI8BK);
-                }
-            stage_barrier<63>();
-        }
-#pragma unroll
-        for (int f = 0; f < TM + TN; ++f) read1(0, f, place(0, 0));
-        uint32_t buf = 0;
-        int kt = 0;
-        if constexpr (DIRECT) {
+            read_first();
             // `left`: stages whose loads may be out when the next one has
             // landed; k0: the stage to load once this one is in registers
             auto stage = [&](auto left, bool more, bool loads, uint32_t k0) {
@@ -429,8 +419,16 @@ void gemm_i8_stage_kernel(const GemmI8Args a)
             for (; kt + 1 < n; ++kt) stage(std::integral_constant<int, 0>{}, true, false, 0);
             stage(std::integral_constant<int, 0>{}, false, false, 0);
         } else {
-            // the next stage moves from its set to LDS, the set takes the
-            // stage NR further on
+            // stage s waits in set s % NR; the next stage moves from its set
+            // to LDS, the set takes the stage NR further on
+            auto hold = [&](int s) {
+#pragma unroll
+                for (int i = 0; i < LM + LN; ++i) hold1(s % NR, i, (uint32_t)s * kI8BK);
+                __builtin_amdgcn_sched_barrier(0);           // set by set: they are waited for in this order
+            };
+            hold(0);
+#pragma unroll
+            for (int i = 0; i < LM + LN; ++i) put1(0, i, 0);
             auto stage = [&](int rset, bool more, bool loads, int at) {
                 step(0, true, buf, 1, more ? kPut : kNone, buf ^ 1u, 0, rset);
                 step(1, true, buf, 2, loads ? kLoad : kNone, 0, (uint32_t)(at + 1 + NR) * kI8BK, rset);
@@ -439,9 +437,23 @@ void gemm_i8_stage_kernel(const GemmI8Args a)
                 step(1, more, buf ^ 1u, 0, kNone, 0, 0, 0);
                 buf ^= 1u;
             };
-            for (; kt + 2 * NR < n; kt += NR) {
+            // the long run starts from loads without a condition: with one, the
+            // compiler cannot count what is on its way and waits for all of it
+            if (2 * NR < n) {
 #pragma unroll
-                for (int r = 0; r < NR; ++r) stage((r + 1) % NR, true, true, kt + r);
+                for (int s = 1; s <= NR; ++s) hold(s);
+                stage_barrier<63>();
+                read_first();
+                for (; kt + 2 * NR < n; kt += NR) {
+#pragma unroll
+                    for (int r = 0; r < NR; ++r) stage((r + 1) % NR, true, true, kt + r);
+                }
+            } else {
+#pragma unroll
+                for (int s = 1; s <= NR; ++s)
+                    if (s < n) hold(s);
+                stage_barrier<63>();
+                read_first();
             }
             for (; kt < n; kt += NR) {
 #pragma unroll
