@@ -70,7 +70,8 @@ struct QuantTokArgs {
 };
 
 // A token held in registers: G threads with C chunks of 8 elements each, one
-// pass over memory.
+// pass over memory.  Bound by memory: 16384 x 4096 bf16 (201 MB) in 42 us, 4.8
+// TB/s; 27 x 3584 takes 2.2 to 3 us.
 template <int G, int C, bool BF16, bool TAIL>
 __global__ __launch_bounds__(row_block<G>()) void quantize_tokens_kernel(const QuantTokArgs a)
 {
@@ -159,7 +160,10 @@ __device__ __forceinline__ float gemm_i8_value(int acc, float sx, float sw, bool
 }
 
 // A 64 x 64 output tile per 256-thread block: four waves of 32 x 32, K in
-// steps of 64 bytes through registers into LDS.
+// steps of 64 bytes through registers into LDS, blocks striding over the
+// tiles and 64-bit offsets throughout.  It serves what the kernels below do
+// not: rows at 4 MB and more from one another, and more tiles than one launch
+// holds (4096 x 4096 x 3584 takes it 172 us, them 55).
 __global__ __launch_bounds__(kBlock) void gemm_i8_tile_kernel(const GemmI8Args a)
 {
     constexpr int kT = 64, kBK = 64;
@@ -547,6 +551,10 @@ void gemm_i8_stage_kernel(const GemmI8Args a)
 // an eighth of K, and a lane's 16-byte load is its MFMA operand (16 rows x 64
 // bytes per instruction).  The eight partial sums meet in LDS; integer sums
 // are exact, so the split changes nothing.  Up to 16 MT tokens.
+//
+// Bound by the weight's way in: 1 x 4096 x 4096 takes 6.0 us, 2.8 TB/s over a
+// call with its launch, and 8 x 8192 x 8192 15.5 us, 4.3 TB/s, near what a
+// copy reaches.  All 64 KB that a CU has to read are asked for at once.
 //
 // XKIND 0 takes codes; 1 (bf16) and 2 (fp32) take up to FM tokens of
 // activations, held in registers in C chunks of 8 a thread, and every block
