@@ -255,6 +255,7 @@ BwdPlan bwd_plan(int64_t T, int64_t H)
     BwdPlan p = {};
     if (H > kBwdWidth) {
         p.blocks = T / 16 < 1 ? 1 : (T / 16 > kMaxChunks ? kMaxChunks : T / 16);
+        while (!grid_fits(p.blocks, align256((size_t)H))) p.blocks /= 2;      // a column's thread in each chunk
         p.part = align256((size_t)(T * 16));
         p.total = p.part + (size_t)(p.blocks * 2 * H * 4);
         return p;
@@ -407,7 +408,9 @@ int launch_long_norm_bwd(const echo::NormBwdArgs& b, hipStream_t st)
         if ((e = check_launch())) return e;
     }
     if (b.dgate && b.gate_rows > 0) {
-        hipLaunchKernelGGL(echo::norm_bwd_gate_kernel, dim3(cols, b.gate_rows < 32768 ? b.gate_rows : 32768), block, 0, st, b);
+        uint32_t gy = b.gate_rows < 32768 ? b.gate_rows : 32768;              // the kernel strides over the rest
+        while (!grid_fits((int64_t)cols * gy, echo::kBlock)) gy /= 2;
+        hipLaunchKernelGGL(echo::norm_bwd_gate_kernel, dim3(cols, gy), block, 0, st, b);
         if ((e = check_launch())) return e;
     }
     if (a.T > 0 && (b.dx || b.dr)) {
