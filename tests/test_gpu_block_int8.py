@@ -217,6 +217,21 @@ def test_gemm_int8_far_rows(echo, M):
     same_bits(y, torch.from_numpy(ref.gemm_int8(xv.numpy(), s.cpu().numpy(), wv.numpy(), t.cpu().numpy(), None)).bfloat16())
 
 
+def test_gemm_int8_most_channels(echo):
+    """More channels than one launch of the few-token form holds (2^27), three codes each."""
+    N, K = (1 << 27) + 5, 3
+    say("gemm most channels", N)
+    g = torch.Generator(device=DEV).manual_seed(2)
+    x = torch.tensor([[100, -128, 7]], dtype=torch.int8, device=DEV)
+    w = torch.randint(-128, 128, (N, K), generator=g, device=DEV, dtype=torch.int8)
+    sx, sw = torch.full((1,), 0.01, device=DEV), torch.rand(N, generator=g, device=DEV)
+    y = torch.empty(1, N, dtype=torch.bfloat16, device=DEV)
+    echo.echo_gemm_int8(x, K, sx, w, K, sw, None, 1, N, K, y, N, echo.BF16)
+    torch.cuda.synchronize()
+    acc = 100 * w[:, 0].int() - 128 * w[:, 1].int() + 7 * w[:, 2].int()
+    same_bits(y[0], ((acc.float() * sx) * sw).bfloat16())
+
+
 @pytest.mark.parametrize("M", [1, 70])
 def test_gemm_int8_empty_sum_and_bad_scales(echo, M):
     """K = 0 gives the bias; a NaN scale makes its own token (or channel) NaN and no other."""

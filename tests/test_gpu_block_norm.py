@@ -266,6 +266,15 @@ def test_backward_parts(echo, H):
         same_bits(v, full[k])
 
 
+@pytest.mark.parametrize("T,H,gate", [(300001, 24, 0), (70003, 24, 1000), (70003, 20, 1)])
+def test_many_tokens(echo, T, H, gate):
+    """More tokens than the blocks of one round hold, forward and backward."""
+    say("norm many tokens", T, H, gate)
+    c = Case(T, H, gate=gate, beta=0.5)
+    check_forward(echo, c)
+    check_backward(echo, c)
+
+
 def test_backward_repeats_its_bits(echo):
     say("backward repeats")
     c = Case(3000, 768, gate=700)
