@@ -57,7 +57,7 @@ struct NormBwdArgs {
     int chunks;             // blocks of the row kernel, or chunks of tokens
     uint32_t per;           // tokens of a group
     uint32_t groups;        // groups that have tokens
-    int spread;             // one gate row (or none): tokens go round the groups
+    uint32_t spread;        // > 0: groups of a gate row (of all tokens without a gate), which go round its tokens
     uint32_t gate_rows;
 };
 
@@ -404,6 +404,8 @@ __global__ __launch_bounds__(kBlock) void norm_bwd_apply_kernel(const NormBwdArg
 //    once; one that a group shares with others goes to that group's slot 0
 //    (its first gate row) or 1 (its last).  A block whose tokens all share
 //    one gate row adds its groups up in LDS and uses its first slot only.
+// Where each gate row can have whole blocks of its own, its tokens go round
+// their groups instead of in runs.
 // Three reductions a token: sum x^2; sum r'^2 with sum dh w_pre r'; and
 // sum dz w_post x.
 //
@@ -426,12 +428,15 @@ __global__ __launch_bounds__(row_block<G>()) void block_norm_bwd_kernel(const No
         t0 = __builtin_amdgcn_readfirstlane(t0);
         t1 = __builtin_amdgcn_readfirstlane(t1);
     }
-    // Where no gate row ends, neighbouring tokens go to neighbouring groups,
-    // so that the chip works on one stretch of memory at a time.
-    const uint32_t step = b.spread ? b.groups : 1;
+    // Spread: neighbouring tokens go to neighbouring groups, each gate row to
+    // groups of its own, so that the chip works on few stretches of memory at
+    // a time (one without a gate).  A block's groups then share a gate row.
+    const uint32_t step = b.spread ? b.spread : 1;
     if (b.spread) {
-        t0 = min((uint32_t)group, (uint32_t)a.T);
-        t1 = group < b.groups ? (uint32_t)a.T : t0;
+        const uint32_t span = a.gate ? a.gate_tokens : (uint32_t)a.T;
+        const int64_t r0 = (group / b.spread) * (int64_t)span;
+        t1 = (uint32_t)min(a.T, r0 + span);
+        t0 = (uint32_t)min((int64_t)t1, r0 + group % b.spread);
     }
     const float invH = 1.0f / (float)a.H;
     float s_post[C][8], s_pre[C][8], sum[C][8], w[C][8], w_pre[C][8];   // w: beta gate w_post
@@ -449,7 +454,8 @@ __global__ __launch_bounds__(row_block<G>()) void block_norm_bwd_kernel(const No
     // whole block on one gate row (its dgate is then left to the block's end)
     const uint32_t bt0 = (uint32_t)min(a.T, (int64_t)blockIdx.x * kGroups * b.per);
     const uint32_t bt1 = (uint32_t)min(a.T, ((int64_t)blockIdx.x + 1) * kGroups * b.per);
-    const bool one_row = a.gate && a.gate_tokens > 1 && bt1 > bt0 && bt0 / a.gate_tokens == (bt1 - 1) / a.gate_tokens;
+    const bool one_row = a.gate && (b.spread ? true : a.gate_tokens > 1 && bt1 > bt0 &&
+                                                          bt0 / a.gate_tokens == (bt1 - 1) / a.gate_tokens);
     // dw_post takes up the sum of a gate row (or of all tokens), the sum becomes dgate
     auto close = [&](const void* gate, int64_t row) {
 #pragma unroll
@@ -632,6 +638,17 @@ __global__ __launch_bounds__(64 * kSumWaves) void norm_bwd_sum_kernel(const Norm
             for (int k = wave; k < b.chunks; k += kSumWaves) s += b.part[(int64_t)(2 * k + blockIdx.y) * a.H + c];
         }
         finish(s, to + c);
+        return;
+    }
+    if (b.spread) {                                          // each block's first slot holds its sum
+        const uint32_t row = blockIdx.y - 2;
+        float s = 0.0f;
+        if (c < a.H) {
+#pragma unroll 8
+            for (uint32_t k = wave; k < b.spread >> group_shift; k += kSumWaves)
+                s += b.gpart[2 * ((int64_t)row * b.spread + ((int64_t)k << group_shift)) * a.H + c];
+        }
+        finish(s, b.dgate + (int64_t)row * b.ld_dgate + c);
         return;
     }
     const uint32_t block_tokens = b.per << group_shift;      // 1 << group_shift groups a block

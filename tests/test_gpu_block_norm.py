@@ -249,6 +249,14 @@ def test_backward_gate_rows_across_blocks(echo, T, gate, H):
     check_backward(echo, Case(T, H, gate=gate, beta=0.5))
 
 
+@pytest.mark.parametrize("T,gate", [(4096, 1024), (4000, 1024), (2050, 2049), (2049, 1024)])
+@pytest.mark.parametrize("H", [100, 700, 1536, 2500, 5000])
+def test_backward_gate_rows_of_their_own_blocks(echo, T, gate, H):
+    """Gate rows long enough for whole blocks each, even and with a short last one, in every width's form."""
+    say("backward own blocks", T, gate, H)
+    check_backward(echo, Case(T, H, gate=gate, beta=0.5))
+
+
 @pytest.mark.parametrize("H", [512, 1001, 17000])
 def test_backward_parts(echo, H):
     """Either gradient alone coming in; any output left out; dr over dr_out; each bit for bit what the full call gives."""
