@@ -292,6 +292,15 @@ uint32_t norm_spread(const BwdPlan& p, int64_t T, int64_t rows, int64_t gate_tok
     return n > 0 && (gate_tokens + n - 1) / n * 8 <= p.per * 9 ? (uint32_t)n : 0;
 }
 
+// Tokens of a gate row that there are (gate_tokens may be any number from 1
+// on), and the gate rows of T tokens.  The first bounds the second's sums:
+// T + gate_tokens does not fit 64 bits for the largest gate_tokens.
+int64_t gate_span(int64_t T, int64_t gate_tokens) { return gate_tokens < T ? gate_tokens : T; }
+int64_t gate_row_count(int64_t T, int64_t gate_tokens)
+{
+    return T > 0 ? (T - 1) / gate_span(T, gate_tokens) + 1 : 0;
+}
+
 int check_norm(const echo_norm_args* p, bool backward)
 {
     if (!p) return ECHO_EINVAL;
@@ -308,7 +317,7 @@ int check_norm(const echo_norm_args* p, bool backward)
     if (!a.post && a.w_post) return ECHO_EINVAL;
     if (a.gate) {
         if (a.gate_tokens < 1) return ECHO_EINVAL;
-        if (bad_ld(a.ld_gate, (a.T + a.gate_tokens - 1) / a.gate_tokens, a.H)) return ECHO_ESHAPE;
+        if (bad_ld(a.ld_gate, gate_row_count(a.T, a.gate_tokens), a.H)) return ECHO_ESHAPE;
     }
     if (a.T == 0 || a.H == 0) return ECHO_OK;   // nothing to read or write: pointers may be NULL
     if (!backward && !a.r_out && !a.h) return ECHO_EINVAL;
@@ -331,7 +340,7 @@ echo::NormArgs norm_args(const echo_norm_args& a)
     n.x = a.x; n.r = a.r; n.w_post = a.w_post; n.w_pre = a.w_pre; n.gate = a.gate;
     n.r_out = a.r_out; n.h = a.h; n.h_scale = a.h_scale;
     n.T = a.T; n.ld_x = a.ld_x; n.ld_r = a.ld_r; n.ld_r_out = a.ld_r_out; n.ld_h = a.ld_h; n.ld_gate = a.ld_gate;
-    n.gate_tokens = (uint32_t)(a.gate_tokens < a.T ? a.gate_tokens : a.T);
+    n.gate_tokens = (uint32_t)gate_span(a.T, a.gate_tokens);
     n.H = (int)a.H;
     n.x_bf16 = a.x_dtype == ECHO_BF16; n.r_bf16 = a.r_dtype == ECHO_BF16; n.w_bf16 = a.w_dtype == ECHO_BF16;
     n.h_kind = a.h_dtype; n.post = a.post;
@@ -535,7 +544,7 @@ int echo_block_norm_backward(const echo_norm_args* p, const echo_norm_grads* gp,
     if ((g.dh && bad_ld(g.ld_dh, T, H)) || (g.dr_out && bad_ld(g.ld_dr_out, T, H)) || (g.dx && bad_ld(g.ld_dx, T, H)) ||
         (g.dr && bad_ld(g.ld_dr, T, H)))
         return ECHO_ESHAPE;
-    const int64_t rows = p->gate ? (T + p->gate_tokens - 1) / p->gate_tokens : 0;
+    const int64_t rows = p->gate ? gate_row_count(T, p->gate_tokens) : 0;
     if (g.dgate && bad_ld(g.ld_dgate, rows, H)) return ECHO_ESHAPE;
     if ((g.dgate && !p->gate) || (g.dw_post && !p->post) || (g.dr && !p->r)) return ECHO_EINVAL;
     if (H == 0) return ECHO_OK;
