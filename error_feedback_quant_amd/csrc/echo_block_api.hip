@@ -253,6 +253,7 @@ constexpr int64_t kMaxChunks = 256;
 BwdPlan bwd_plan(int64_t T, int64_t H)
 {
     BwdPlan p = {};
+    if (T == 0) return p;                               // the sums' kernels then write zeros
     if (H > kBwdWidth) {
         p.blocks = T / 16 < 1 ? 1 : (T / 16 > kMaxChunks ? kMaxChunks : T / 16);
         while (!grid_fits(p.blocks, align256((size_t)H))) p.blocks /= 2;      // a column's thread in each chunk
@@ -271,7 +272,7 @@ BwdPlan bwd_plan(int64_t T, int64_t H)
     if (most < kCus) most = kCus;
     most <<= p.group_shift;
     const int64_t groups = (T + 1) / 2 < most ? (T + 1) / 2 : most;
-    p.per = groups ? (T + groups - 1) / groups : 1;
+    p.per = (T + groups - 1) / groups;
     p.groups = (T + p.per - 1) / p.per;
     p.blocks = (p.groups + (1 << p.group_shift) - 1) >> p.group_shift;
     p.gpart = align256((size_t)(p.blocks * 2 * H * 4));
@@ -286,7 +287,7 @@ BwdPlan bwd_plan(int64_t T, int64_t H)
 // gate rows of 2048 305 and 321.
 uint32_t norm_spread(const BwdPlan& p, int64_t T, int64_t rows, int64_t gate_tokens)
 {
-    if (p.groups == 0) return 0;
+    if (p.groups == 0) return 0;                        // no tokens, or a width without groups
     if (rows <= 1) return (uint32_t)(p.blocks << p.group_shift);
     const int64_t n = ((p.blocks << p.group_shift) / rows >> p.group_shift) << p.group_shift;
     return n > 0 && (gate_tokens + n - 1) / n * 8 <= p.per * 9 ? (uint32_t)n : 0;
@@ -424,8 +425,10 @@ int launch_long_norm_bwd(const echo::NormBwdArgs& b, hipStream_t st)
         if ((e = check_launch())) return e;
     }
     if (b.dw_post || b.dw_pre) {
-        hipLaunchKernelGGL(echo::norm_bwd_weights_kernel, dim3(cols, (unsigned)b.chunks), block, 0, st, b);
-        if ((e = check_launch())) return e;
+        if (b.chunks) {
+            hipLaunchKernelGGL(echo::norm_bwd_weights_kernel, dim3(cols, (unsigned)b.chunks), block, 0, st, b);
+            if ((e = check_launch())) return e;
+        }
         hipLaunchKernelGGL(echo::norm_bwd_weights_sum_kernel, dim3(cols), block, 0, st, b);
         if ((e = check_launch())) return e;
     }

@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import _launches
+from error_feedback_quant_amd import echo
 
 pytestmark = [pytest.mark.skipif(torch.cuda.is_available(), reason="host-only: launches are recorded, not made"),
               pytest.mark.skipif(shutil.which("gcc") is None, reason="needs gcc")]
@@ -49,3 +50,16 @@ def test_gate_rows_of_any_length(recorder, T, H):
                 assert join[0][1][1] == 2 + 1, (n, got)
             else:
                 assert 2 <= join[0][1][1] <= 2 + rows, (n, got)
+
+
+@pytest.mark.parametrize("H", [64, 8192, 8193, 9000, 20000])
+def test_no_tokens_make_one_launch(recorder, H):
+    """Without tokens only the sums' kernel runs (it writes the weights' zero gradients), without a workspace."""
+    (rc, got), (rc_gate, got_gate), (rc_none, got_none) = _launches.backward_launches(
+        recorder, [dict(T=0, H=H), dict(T=0, H=H, gate_tokens=7, gate=True), dict(T=0, H=H, dw=False)])
+    assert rc == 0 and rc_gate == 0 and rc_none == 0
+    for g in (got, got_gate):
+        check_dims(g)
+        assert len(g) == 1 and "sum_kernel" in g[0][0], g
+    assert not got_none
+    assert echo.echo_block_norm_backward_workspace_bytes(0, H) == 0

@@ -38,3 +38,16 @@ def test_one_gate_row_for_any_number_of_tokens(echo, T, H, gate):
     for k, v in got.items():
         same_bits(v, want[k])
     same_bits(hg, h)
+
+
+@pytest.mark.parametrize("H", [64, 8192, 8193, 20000])
+def test_no_tokens_at_every_width(echo, H):
+    """No tokens: the weights' gradients are zeros, whichever form the width takes."""
+    say("no tokens", H)
+    x = torch.empty(0, H, device=DEV)
+    dw = torch.full((2, H), 7.0, device=DEV)
+    ws = torch.empty(max(16, echo.echo_block_norm_backward_workspace_bytes(0, H)), dtype=torch.uint8, device=DEV)
+    echo.echo_block_norm_backward(echo.make_norm_args(x, x), echo.make_norm_grads(
+        dh=x, dr_out=x, dx=x, dr=x, dw_post=dw[0], dw_pre=dw[1], workspace=ws))
+    torch.cuda.synchronize()
+    assert not bool(dw.any())
