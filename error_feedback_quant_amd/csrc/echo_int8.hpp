@@ -19,6 +19,7 @@
 
 #include "echo_kernels.hpp"
 #include "echo_rows.hpp"
+#include "echo_stage.hpp"
 
 namespace echo {
 
@@ -249,10 +250,6 @@ __device__ __forceinline__ void xcd_tile_of(uint32_t b, uint32_t tiles_m, uint32
     tn = in / rows;
 }
 
-// 16-byte chunk c of stage row r lies at chunk c ^ key(r): the rows of a
-// fragment (one row per lane, 128 bytes apart) then start on distinct banks
-__device__ __forceinline__ uint32_t i8_key(uint32_t r) { return (r & 7u) ^ ((r >> 3) & 1u); }
-
 // s_waitcnt operand: at most `left` vector-memory operations outstanding
 constexpr int waitcnt_vm(int left) { return 0x0F70 | (left & 15) | ((left >> 4) << 14); }
 
@@ -266,6 +263,12 @@ __device__ __forceinline__ void stage_barrier()
     __builtin_amdgcn_s_waitcnt(waitcnt_vm(LEFT) & 0xF0FF);
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+}
+
+// 16 bytes of each lane from its offset, behind k0, to 16 bytes a lane of LDS
+__device__ __forceinline__ void stage_load16(__amdgpu_buffer_rsrc_t r, uint32_t off, uint32_t k0, uint8_t* lds)
+{
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 16, off, k0, 0, 0);
 }
 
 template <int BM, int BN, int WM, int WN, int NS, int NR>
@@ -292,7 +295,6 @@ void gemm_i8_stage_kernel(const GemmI8Args a)
     const int8_t* px = a.x + m0 * a.ldx;
     const int8_t* pw = a.w + n0 * a.ldw;
     const uint32_t ldx = (uint32_t)a.ldx, ldw = (uint32_t)a.ldw;
-    // a row past the last valid one lies past the record count and reads as 0
     const __amdgpu_buffer_rsrc_t rx =
         __builtin_amdgcn_make_buffer_rsrc((void*)px, (short)0, (int)((rows_m - 1) * ldx + a.K), 0x00020000);
     const __amdgpu_buffer_rsrc_t rw =
@@ -302,22 +304,24 @@ void gemm_i8_stage_kernel(const GemmI8Args a)
     // base, so it fetches the chunk that belongs there
     const uint32_t lrow = wave * 8 + (lane >> 3);
     const uint32_t lchunk = (lane & 7u) ^ i8_key(lrow);
-    const uint32_t offx = lrow * ldx + 16 * lchunk, offw = lrow * ldw + 16 * lchunk;
-    auto issue1 = [&](int i, uint32_t buf, uint32_t k0) {    // load i of a stage: LM of x, then LN of w
+    uint32_t off[LM + LN];                                   // of a stage's loads: LM of x, then LN of w
+#pragma unroll
+    for (int i = 0; i < LM + LN; ++i) {
+        const uint32_t r = lrow + 8 * NW * (i < LM ? i : i - LM);
+        off[i] = i < LM ? stage_offset(r, (uint32_t)rows_m, ldx, lchunk) : stage_offset(r, (uint32_t)rows_n, ldw, lchunk);
+    }
+    auto issue1 = [&](int i, uint32_t buf, uint32_t k0) {
         uint8_t* to = smem + buf * kStage + (i < LM ? 0 : BM * kI8BK);
         const int j = i < LM ? i : i - LM;
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            i < LM ? rx : rw, (__attribute__((address_space(3))) void*)(to + (8 * NW * j + wave * 8) * kI8BK), 16,
-            i < LM ? offx : offw, k0 + (uint32_t)(8 * NW * j) * (i < LM ? ldx : ldw), 0, 0);
+        stage_load16(i < LM ? rx : rw, off[i], k0, to + (8 * NW * j + wave * 8) * kI8BK);
     };
     auto issue = [&](uint32_t buf, uint32_t k0) {
 #pragma unroll
         for (int i = 0; i < LM + LN; ++i) issue1(i, buf, k0);
     };
-    // The same through NR sets of registers, for rows that start anywhere.  A
-    // row past the last valid one repeats it.  The words that hold the 16
-    // bytes are loaded and shifted together: 16-byte loads at odd addresses
-    // ran at under half the rate.
+    // The same through NR sets of registers, for rows that start anywhere.  The
+    // words that hold the 16 bytes are loaded and shifted together: 16-byte
+    // loads at odd addresses ran at under half the rate.
     constexpr int kSets = DIRECT ? 1 : NR, kHeld = DIRECT ? 1 : LM + LN;
     u32x4 held[kSets][kHeld];
     uint32_t last[kSets][kHeld], hoff[kHeld], hshift[kHeld];
@@ -342,10 +346,8 @@ void gemm_i8_stage_kernel(const GemmI8Args a)
     if constexpr (!DIRECT) {
 #pragma unroll
         for (int i = 0; i < LM + LN; ++i) {
-            const uint32_t r = lrow + 8 * NW * (i < LM ? i : i - LM);
-            const uint32_t off = (i < LM ? min(r, (uint32_t)rows_m - 1) * ldx : min(r, (uint32_t)rows_n - 1) * ldw) + 16 * lchunk;
-            hshift[i] = (uint32_t)((uintptr_t)(i < LM ? px : pw) + off) & 3u;
-            hoff[i] = off - hshift[i];                       // down to the word; -3 at the least
+            hshift[i] = (uint32_t)((uintptr_t)(i < LM ? px : pw) + off[i]) & 3u;
+            hoff[i] = off[i] - hshift[i];                    // down to the word; -3 at the least
         }
     }
 
