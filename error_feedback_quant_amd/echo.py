@@ -340,6 +340,7 @@ def make_norm_args(x, r=None, r_out=None, h=None, h_scale=None, post=True, w_pos
     if gate is not None:
         if gate_tokens < 1:
             raise ValueError("a gate needs gate_tokens >= 1")
+        gate_tokens = min(gate_tokens, max(T, 1))          # a field of 64 bits
         pg, ld_g, _ = _rows(gate, (-(-T // gate_tokens), H), "gate", (kw,))
     else:
         gate_tokens = 0
