@@ -73,10 +73,28 @@ __device__ __forceinline__ float block_sum(float v, float* red)
     return v;
 }
 
+// rsqrt(mean + eps) of a row from its sum of squares; 0 where that left fp32
 __device__ __forceinline__ float norm_factor(float sum_sq, int H, float eps)
 {
     return 1.0f / __builtin_sqrtf(sum_sq / (float)H + eps);
 }
+// Squares leave fp32 long before the values do (from about 2^64 / sqrt(H) on),
+// and a factor of 0 would let the row vanish: such a row is summed again by
+// `scaled_sum`, over its values times kNormSmall (2^30 squares of 2^48 at the
+// most).  A row that holds an infinity or a NaN has the factor NaN, so that
+// none of its normed values passes for a number.
+constexpr float kNormSmall = 0x1p-80f;
+template <typename F>
+__device__ __forceinline__ float norm_factor(float sum_sq, int H, float eps, F scaled_sum)
+{
+    if (__builtin_expect(sum_sq / (float)H + eps < __builtin_inff(), 1)) return norm_factor(sum_sq, H, eps);
+    const float m = scaled_sum() / (float)H + eps * kNormSmall * kNormSmall;
+    return m < __builtin_inff() ? kNormSmall / __builtin_sqrtf(m) : __builtin_nanf("");
+}
+// Backward, tokens with a smaller factor than this take a way of their own: a
+// product of three factors, or a sum of values times gradients, may leave
+// fp32 where the results do not.
+constexpr float kNormLeast = 0x1p-40f;
 
 // one element's place in the formulas
 struct NormElem {
@@ -170,7 +188,14 @@ __global__ __launch_bounds__(row_block<G>()) void block_norm_kernel(const NormAr
             for (int j = 0; j < C; ++j)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) s = fmaf(raw_get(x[j], e), raw_get(x[j], e), s);
-            kx = norm_factor(row_sum<G>(s, red, turn++), a.H, a.eps);
+            kx = norm_factor(row_sum<G>(s, red, turn++), a.H, a.eps, [&] {
+                float b = 0.0f;
+#pragma unroll
+                for (int j = 0; j < C; ++j)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) b = fmaf(raw_get(x[j], e) * kNormSmall, raw_get(x[j], e) * kNormSmall, b);
+                return row_sum<G>(b, red, turn++);
+            });
         }
         float v[C][8];
         float s = 0.0f;
@@ -184,7 +209,14 @@ __global__ __launch_bounds__(row_block<G>()) void block_norm_kernel(const NormAr
             if (a.r_out) st_row8<RB, TAIL>(a.r_out, t * a.ld_r_out, 8 * (g + G * j), a.H, v[j]);
         }
         if (!a.h) continue;
-        const float kr = norm_factor(row_sum<G>(s, red, turn++), a.H, a.eps);
+        const float kr = norm_factor(row_sum<G>(s, red, turn++), a.H, a.eps, [&] {
+            float b = 0.0f;
+#pragma unroll
+            for (int j = 0; j < C; ++j)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) b = fmaf(v[j][e] * kNormSmall, v[j][e] * kNormSmall, b);
+            return row_sum<G>(b, red, turn++);
+        });
 #pragma unroll
         for (int j = 0; j < C; ++j)
 #pragma unroll
@@ -215,6 +247,21 @@ __global__ __launch_bounds__(row_block<G>()) void block_norm_kernel(const NormAr
     }
 }
 
+// Factor of a row that a block walks over: value(c) is its element c
+template <typename F>
+__device__ __forceinline__ float row_factor(const NormArgs& a, float* red, F value)
+{
+    auto sum = [&](float scale) {
+        float s = 0.0f;
+        for (int c = threadIdx.x; c < a.H; c += kBlock) {
+            const float v = value(c) * scale;
+            s = fmaf(v, v, s);
+        }
+        return block_sum(s, red);
+    };
+    return norm_factor(sum(1.0f), a.H, a.eps, [&] { return sum(kNormSmall); });
+}
+
 // Rows too wide for registers: one block per token of any width, the row read
 // again in each pass (from L2 where it fits).
 __global__ __launch_bounds__(kBlock) void block_norm_any_kernel(const NormArgs a)
@@ -223,23 +270,11 @@ __global__ __launch_bounds__(kBlock) void block_norm_any_kernel(const NormArgs a
     __shared__ uint32_t redu[kBlock / 64];
     for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
         float kx = 0.0f;
-        if (a.post) {
-            float s = 0.0f;
-            for (int c = threadIdx.x; c < a.H; c += kBlock) {
-                const float v = ld_elem(a.x, a.x_bf16, t * a.ld_x + c);
-                s = fmaf(v, v, s);
-            }
-            kx = norm_factor(block_sum(s, red), a.H, a.eps);
-        }
+        if (a.post) kx = row_factor(a, red, [&](int c) { return ld_elem(a.x, a.x_bf16, t * a.ld_x + c); });
         float kr = 0.0f;
         TokenScale q = {0.0f, 0.0f};
         if (a.h) {
-            float s = 0.0f;
-            for (int c = threadIdx.x; c < a.H; c += kBlock) {
-                const float v = norm_elem(a, t, c, kx).r;
-                s = fmaf(v, v, s);
-            }
-            kr = norm_factor(block_sum(s, red), a.H, a.eps);
+            kr = row_factor(a, red, [&](int c) { return norm_elem(a, t, c, kx).r; });
             if (a.h_kind == ECHO_I8) {
                 uint32_t m = 0;
                 for (int c = threadIdx.x; c < a.H; c += kBlock) {
@@ -295,19 +330,9 @@ __global__ __launch_bounds__(kBlock) void norm_bwd_stats_kernel(const NormBwdArg
     __shared__ float red[kBlock / 64];
     const NormArgs& a = b.f;
     for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+        const float kx = row_factor(a, red, [&](int c) { return ld_elem(a.x, a.x_bf16, t * a.ld_x + c); });
+        const float kr = row_factor(a, red, [&](int c) { return norm_elem(a, t, c, kx).r; });
         float s = 0.0f;
-        for (int c = threadIdx.x; c < a.H; c += kBlock) {
-            const float v = ld_elem(a.x, a.x_bf16, t * a.ld_x + c);
-            s = fmaf(v, v, s);
-        }
-        const float kx = norm_factor(block_sum(s, red), a.H, a.eps);
-        s = 0.0f;
-        for (int c = threadIdx.x; c < a.H; c += kBlock) {
-            const float v = norm_elem(a, t, c, kx).r;
-            s = fmaf(v, v, s);
-        }
-        const float kr = norm_factor(block_sum(s, red), a.H, a.eps);
-        s = 0.0f;
         for (int c = threadIdx.x; c < a.H; c += kBlock) {
             const NormGrad g = norm_grad(b, t, c, kx, kr, 0.0f);
             s = fmaf(g.dhw, g.n_r, s);
@@ -421,7 +446,8 @@ __global__ __launch_bounds__(row_block<G>()) void block_norm_bwd_kernel(const No
     __shared__ __align__(8) float red[G > 64 ? 6 * G / 64 : 2];
     __shared__ float meet[kGroups > 1 ? (kGroups - 1) * G * C * 8 : 1];
     const NormArgs& a = b.f;
-    const int g = threadIdx.x % G, q = threadIdx.x / G;
+    int g = threadIdx.x % G;
+    const int q = threadIdx.x / G;
     const int64_t group = (int64_t)blockIdx.x * kGroups + q;
     uint32_t t0 = (uint32_t)min(a.T, group * b.per), t1 = (uint32_t)min(a.T, (group + 1) * b.per);
     if constexpr (G == 64) {
@@ -457,7 +483,7 @@ __global__ __launch_bounds__(row_block<G>()) void block_norm_bwd_kernel(const No
     const bool one_row = a.gate && (b.spread ? true : a.gate_tokens > 1 && bt1 > bt0 &&
                                                           bt0 / a.gate_tokens == (bt1 - 1) / a.gate_tokens);
     // dw_post takes up the sum of a gate row (or of all tokens), the sum becomes dgate
-    auto close = [&](const void* gate, int64_t row) {
+    auto close = [&](const void* gate, int64_t row, float (&sum)[C][8]) {
 #pragma unroll
         for (int j = 0; j < C; ++j) {
             float v[8];
@@ -473,15 +499,16 @@ __global__ __launch_bounds__(row_block<G>()) void block_norm_bwd_kernel(const No
 #pragma unroll
         for (int j = 0; j < C; ++j) st_row8<false, TAIL>(to, row, 8 * (g + G * j), a.H, v[j]);
     };
-    // the gate row that ends (for this group) at token `end`
+    // the gate row that ends (for this group) at token `end`; f(array, row in it) stores its sum
+    auto place = [&](uint32_t row, uint32_t end, auto f) {
+        const uint64_t r0 = (uint64_t)row * a.gate_tokens;
+        const bool whole = r0 >= t0 && (r0 + a.gate_tokens <= end || end == (uint32_t)a.T);
+        if (whole) f(b.dgate, (int64_t)row * b.ld_dgate);
+        else f(b.gpart, (2 * group + (r0 > t0 ? 1 : 0)) * (int64_t)a.H);
+    };
     auto flush = [&](uint32_t row, uint32_t end) {
-        close(a.gate, (int64_t)row * a.ld_gate);
-        if (b.dgate && !one_row) {
-            const uint64_t r0 = (uint64_t)row * a.gate_tokens;
-            const bool whole = r0 >= t0 && (r0 + a.gate_tokens <= end || end == (uint32_t)a.T);
-            if (whole) put(b.dgate, (int64_t)row * b.ld_dgate, sum);
-            else put(b.gpart, (2 * group + (r0 > t0 ? 1 : 0)) * (int64_t)a.H, sum);
-        }
+        close(a.gate, (int64_t)row * a.ld_gate, sum);
+        if (b.dgate && !one_row) place(row, end, [&](float* to, int64_t at) { put(to, at, sum); });
     };
 
     Raw8<XB> x[C], nx[C];
@@ -499,6 +526,7 @@ __global__ __launch_bounds__(row_block<G>()) void block_norm_bwd_kernel(const No
     };
     uint32_t gate_row = ~0u;
     int turn = 0;
+    bool far = false;
     if (t0 < t1) load(t0);
     for (uint32_t t = t0; t < t1; t += step) {
 #pragma unroll
@@ -539,8 +567,14 @@ __global__ __launch_bounds__(row_block<G>()) void block_norm_bwd_kernel(const No
             }
         row_sum2<G>(s, p, red + (G > 64 ? 2 * G / 64 : 0), turn);
         ++turn;
-        const float kr = norm_factor(s, a.H, a.eps);
-        const float km = p * kr * invH * kr;                 // k_r mean(dh w_pre n_r)
+        float kr = norm_factor(s, a.H, a.eps);
+        // A token left to the loop below adds zeros here, with factors of 0,
+        // and is not stored (a branch around the rest costs registers).
+        const bool near = kx >= kNormLeast && kr >= kNormLeast;
+        far |= !near;
+        const float km = near ? p * kr * invH * kr : 0.0f;   // k_r mean(dh w_pre n_r)
+        kx = near ? kx : 0.0f;
+        kr = near ? kr : 0.0f;
         float o = 0.0f;
 #pragma unroll
         for (int j = 0; j < C; ++j)
@@ -552,7 +586,7 @@ __global__ __launch_bounds__(row_block<G>()) void block_norm_bwd_kernel(const No
                 sum[j][e] = fmaf(v[j][e], xe * kx, sum[j][e]);
                 o = fmaf(v[j][e] * w[j][e], xe, o);
             }
-        if (b.dr) {
+        if (b.dr && near) {
 #pragma unroll
             for (int j = 0; j < C; ++j) {
                 float y[8];
@@ -561,7 +595,7 @@ __global__ __launch_bounds__(row_block<G>()) void block_norm_bwd_kernel(const No
                 st_row8<RB, TAIL>(b.dr, (int64_t)t * b.ld_dr, 8 * (g + G * j), a.H, y);
             }
         }
-        if (b.dx) {
+        if (b.dx && near) {
             float mx = 0.0f;                                 // k_x^2 mean(dz w_post n_x)
             if (a.post) mx = row_sum<G>(o, red, turn++) * kx * invH * kx * kx;
 #pragma unroll
@@ -573,8 +607,126 @@ __global__ __launch_bounds__(row_block<G>()) void block_norm_bwd_kernel(const No
             }
         }
     }
-    if (!a.gate) close(nullptr, 0);
+    if (!a.gate) close(nullptr, 0, sum);
     else if (gate_row != ~0u) flush(gate_row, t1);
+
+    // Tokens of values too large for the products above, or of some that are no
+    // numbers: the same gradients from their normed values, added to the sums
+    // above.  In a loop of its own after those are done, because in the loop
+    // above it costs that one registers (8000 rows of 8192 in fp32: 492 us, 315
+    // here).  g is made opaque at each use, or the addresses that both loops
+    // work out of it are kept, and spilled, from the kernel's start on.
+    if (far) {
+        asm("" : "+v"(g));
+        float more[C][8];
+        auto clear = [&] {
+#pragma unroll
+            for (int j = 0; j < C; ++j)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) more[j][e] = 0.0f;
+        };
+        auto join = [&](uint32_t row, uint32_t end) {
+            close(a.gate, (int64_t)row * a.ld_gate, more);
+            if (b.dgate && one_row) {
+#pragma unroll
+                for (int j = 0; j < C; ++j)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) sum[j][e] += more[j][e];
+            } else if (b.dgate) {
+                place(row, end, [&](float* to, int64_t at) {
+#pragma unroll
+                    for (int j = 0; j < C; ++j) {
+                        const Raw8<false> had = ld_raw8<false, TAIL>(to, at, 8 * (g + G * j), a.H);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) more[j][e] += raw_get(had, e);
+                    }
+                    put(to, at, more);
+                });
+            }
+            clear();
+        };
+        clear();
+        gate_row = ~0u;
+        for (uint32_t t = t0; t < t1; t += step) {
+            asm("" : "+v"(g));
+            if (a.gate) {
+                const uint32_t row = t / a.gate_tokens;
+                if (row != gate_row) {
+                    if (gate_row != ~0u) join(gate_row, t);
+                    weights(a.gate, (int64_t)row * a.ld_gate);
+                    gate_row = row;
+                }
+            }
+            float v[C][8], kx = 1.0f, kr;
+            // the loop's own factor, by which it left the token out, and the one that holds for large values
+            auto factor = [&](auto value, float& k) {
+                auto sum_sq = [&](float scale) {
+                    float q = 0.0f, none = 0.0f;
+#pragma unroll
+                    for (int j = 0; j < C; ++j)
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) q = fmaf(value(j, e) * scale, value(j, e) * scale, q);
+                    row_sum2<G>(q, none, red + (G > 64 ? 2 * G / 64 : 0), turn++);
+                    return q;
+                };
+                const float q = sum_sq(1.0f);
+                k = norm_factor(q, a.H, a.eps, [&] { return sum_sq(kNormSmall); });
+                return !(norm_factor(q, a.H, a.eps) >= kNormLeast);
+            };
+            bool is_far = false;
+#pragma unroll
+            for (int j = 0; j < C; ++j) x[j] = ld_raw8<XB, TAIL>(a.x, (int64_t)t * a.ld_x, 8 * (g + G * j), a.H);
+            if (a.post) is_far = factor([&](int j, int e) { return raw_get(x[j], e); }, kx);
+#pragma unroll
+            for (int j = 0; j < C; ++j) {
+                r[j] = ld_raw8<RB, TAIL>(a.r, (int64_t)t * a.ld_r, 8 * (g + G * j), a.r ? a.H : 0);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[j][e] = fmaf(raw_get(x[j], e) * kx, w[j][e], a.rho * raw_get(r[j], e));
+            }
+            is_far |= factor([&](int j, int e) { return v[j][e]; }, kr);
+            if (!is_far) continue;
+            float s = 0.0f;
+#pragma unroll
+            for (int j = 0; j < C; ++j) {
+                dh[j] = ld_raw8<HB, TAIL>(b.dh, (int64_t)t * b.ld_dh, 8 * (g + G * j), b.dh ? a.H : 0);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    v[j][e] *= kr;                           // n_r, then d
+                    s = fmaf(raw_get(dh[j], e) * w_pre[j][e], v[j][e], s);
+                }
+            }
+            const float m = row_sum<G>(s, red, turn++) * invH;
+            s = 0.0f;
+#pragma unroll
+            for (int j = 0; j < C; ++j) {
+                float y[8];
+                up[j] = ld_raw8<RB, TAIL>(b.dr_out, (int64_t)t * b.ld_dr_out, 8 * (g + G * j), b.dr_out ? a.H : 0);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float n = v[j][e], h = raw_get(dh[j], e), n_x = raw_get(x[j], e) * kx;
+                    s_pre[j][e] = fmaf(h, n, s_pre[j][e]);
+                    v[j][e] = fmaf(kr, fmaf(h, w_pre[j][e], -n * m), raw_get(up[j], e));
+                    y[e] = a.rho * v[j][e];
+                    more[j][e] = fmaf(v[j][e], n_x, more[j][e]);
+                    v[j][e] *= w[j][e];
+                    s = fmaf(v[j][e], n_x, s);
+                }
+                if (b.dr) st_row8<RB, TAIL>(b.dr, (int64_t)t * b.ld_dr, 8 * (g + G * j), a.H, y);
+            }
+            if (!b.dx) continue;
+            const float mx = a.post ? row_sum<G>(s, red, turn++) * invH : 0.0f;
+#pragma unroll
+            for (int j = 0; j < C; ++j) {
+                float y[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[e] = kx * fmaf(-(raw_get(x[j], e) * kx), mx, v[j][e]);
+                st_row8<XB, TAIL>(b.dx, (int64_t)t * b.ld_dx, 8 * (g + G * j), a.H, y);
+            }
+        }
+        asm("" : "+v"(g));
+        if (!a.gate) close(nullptr, 0, more);
+        else join(gate_row, t1);
+    }
 
     // sums of the block: group 0 adds the others' from LDS
     auto gather = [&](float (&v)[C][8]) {

@@ -364,9 +364,12 @@ size_t echo_noalloc_scratch_bytes(void);
  *  - Pointers need the alignment of their element type only (workspaces 16
  *    bytes); where the base and ld of every matrix of a call are multiples of
  *    16 bytes the call is fastest.
- *  - Non-finite values: an infinity or a NaN in a token makes results of that
- *    token non-finite and touches no other token (the sums over tokens in a
- *    backward pass take it up).
+ *  - Non-finite values: what is normed, quantized or multiplied from a token
+ *    that holds an infinity or a NaN is NaN throughout (8-bit codes are 0 with
+ *    a scale of NaN), and so are that token's gradients; a residual sum has it
+ *    where it stands.  No other token is touched (the sums over tokens in a
+ *    backward pass take it up).  Finite values are normed by the formulas
+ *    whatever their size, also where their squares leave fp32.
  *  - Inputs and outputs do not overlap except where a call says so.
  */
 
