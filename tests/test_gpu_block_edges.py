@@ -168,3 +168,26 @@ def test_gradients_of_tokens_that_hold_no_number(echo, H, bad):
             assert bool(torch.isnan(got[k][[1, 4]]).all())
         rows = [1, 3, 4]                      # gate rows without such a token
         same_bits(got["dgate"][rows].contiguous(), clean["dgate"][rows].contiguous())
+
+
+@pytest.mark.parametrize("H", [64, 1000, 4096, 8192, 8200, 17000])
+def test_sums_over_many_equal_tokens(echo, H):
+    """60000 equal tokens behind one gate row: the sums are 60000 times one
+    token's gradient.  A chain of T additions would be off by thousands of u
+    (each addition rounds the same way for a while); the longest chain of any
+    form is 235 tokens (60000 over 256 blocks or chunks) and 256 partial sums."""
+    T = 60000
+    say("equal tokens", H)
+    one = Case(1, H, gate=1, beta=0.5)
+    f = one.plain()
+    want, mag = ref.norm_backward(f, ref.f64(one.x), ref.f64(one.dh), None, ref.f64(one.gate), 1, True, one.rho64, one.beta64)
+    c = Case(1, H, gate=1, beta=0.5)
+    c.T = c.gate_tokens = T
+    for k in ("x", "r", "dh", "up"):
+        setattr(c, k, getattr(one, k).repeat(T, 1))
+    got = run_backward(echo, c, up=False, want=("dw_post", "dw_pre", "dgate"))
+    for k in ("dw_post", "dw_pre", "dgate"):
+        tol = (ref.backward_eps(f, H) + 500 * ref.U) * T * mag[k]
+        assert float(np.median(tol / (T * np.abs(want[k]) + 1e-30))) < 2e-3, k       # the bound is a small part of the sum
+        off = np.abs(ref.f64(got[k]) - T * want[k])
+        assert (off <= tol + ref.U * T * np.abs(want[k])).all(), (k, float((off / tol).max()))
