@@ -191,3 +191,125 @@ def test_sums_over_many_equal_tokens(echo, H):
         assert float(np.median(tol / (T * np.abs(want[k]) + 1e-30))) < 2e-3, k       # the bound is a small part of the sum
         off = np.abs(ref.f64(got[k]) - T * want[k])
         assert (off <= tol + ref.U * T * np.abs(want[k])).all(), (k, float((off / tol).max()))
+
+
+def one_signed(c):
+    """Incoming gradients signed so that each column's terms mostly add up:
+    dh along n_r, dr_out along x and above what h's gradient adds to it."""
+    f = c.plain()
+    sign = lambda v: torch.from_numpy(np.where(v < 0, -1.0, 1.0)).to(DEV)  # noqa: E731
+    c.dh.copy_((sign(f["n_r"]) * c.dh.abs().double()).to(c.dh.dtype))
+    c.up.copy_((sign(ref.f64(c.x)) * (4 + c.up.abs().double())).to(c.up.dtype))
+
+
+@pytest.mark.parametrize("T,H,gate", [(300001, 24, 0), (300001, 24, 300001), (70003, 24, 1000), (70003, 20, 7), (70003, 24, 2500),
+                                      (30001, 600, 30001), (20001, 1500, 0), (20001, 2100, 3000), (9001, 4100, 9001)])
+def test_sums_over_many_tokens(echo, T, H, gate):
+    """Sums whose terms have one sign, so that a lost, doubled or unwritten
+    partial sum shows: the bound takes each form's own longest chain (under
+    300 additions: 147 tokens of a group at most, the groups of a block, and
+    a sixteenth of up to 1024 blocks with 16 waves)."""
+    say("sums over many tokens", T, H, gate)
+    c = Case(T, H, gate=gate, beta=0.5)
+    if gate:
+        c.gate.abs_()
+    one_signed(c)
+    f = c.plain()
+    got = run_backward(echo, c)
+    want, mag = ref.norm_backward(f, ref.f64(c.x), ref.f64(c.dh), ref.f64(c.up), ref.f64(c.gate), gate or 1, True, c.rho64,
+                                  c.beta64)
+    for k in ("dw_post", "dw_pre") + (("dgate",) if gate else ()):
+        tol = (ref.backward_eps(f, H) + 300 * ref.U) * mag[k]
+        share = np.quantile(tol / np.abs(want[k]), 0.95)
+        assert share < 5e-4, (k, share)                    # a block's part (a thousandth and more) lies well outside the bound
+        off = np.abs(ref.f64(got[k]) - want[k])
+        assert (off <= tol + ref.U * np.abs(want[k])).all(), (k, float((off / tol).max()))
+
+
+@pytest.mark.parametrize("T,K", [(3, 1025), (40, 1500), (5, 2047), (9, 4095), (3, 4097), (5, 9001), (2, 16383), (3, 16385)])
+@pytest.mark.parametrize("pad,off", [(0, 0), (3, 1)])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_quantize_tokens_that_end_inside_a_chunk(echo, T, K, pad, off, dt):
+    say("quantize tail", T, K, pad, off, dt)
+    d = torch.bfloat16 if dt == "bf16" else torch.float32
+    rng = np.random.default_rng(K)
+    v = torch.from_numpy(rng.standard_normal((T, K)).astype(np.float32))
+    v[0, K - 1], v[-1, 0] = -90.0, 70.0                    # a largest value in the last, partial chunk
+    _, x = matrix(T, K, K + pad, d, v, off)
+    qb, q = matrix(T, K, K + pad, torch.int8, None, off)
+    sb, s = matrix(1, T, T, torch.float32, None, off)
+    echo.echo_quantize_tokens(x, K + pad, echo.BF16 if dt == "bf16" else echo.F32, T, K, q, K + pad, s)
+    torch.cuda.synchronize()
+    wq, ws = ref.quantize_tokens(x.float().cpu().numpy())
+    same_bits(q, torch.from_numpy(wq))
+    same_bits(s[0], torch.from_numpy(ws))
+    untouched(qb, q)
+    untouched(sb, s)
+
+
+@pytest.mark.parametrize("M", [1, 2, 3, 4])
+@pytest.mark.parametrize("N,K", [(40, 4097), (130, 5000), (64, 6144), (33, 8191), (256, 8192), (17, 4104)])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("pad,off", [(0, 0), (8, 0), (5, 1)])
+def test_linear_of_few_long_tokens(echo, M, N, K, dt, pad, off):
+    """One launch with two chunks a thread: the codes and the product bit for bit, without a workspace."""
+    say("linear long", M, N, K, dt, pad, off)
+    d = torch.bfloat16 if dt == "bf16" else torch.float32
+    rng = np.random.default_rng(M * N + K)
+    v = torch.from_numpy(rng.standard_normal((M, K)).astype(np.float32))
+    v[0, K - 1] = 60.0
+    if M > 2:
+        v[1, K // 2] = float("inf")
+    _, x = matrix(M, K, K + pad, d, v, off)
+    wv = torch.from_numpy(rng.integers(-128, 128, (N, K), dtype=np.int64).astype(np.int8))
+    _, w = matrix(N, K, K + pad, torch.int8, wv, off)
+    sw = torch.from_numpy(rng.uniform(0.001, 0.1, N).astype(np.float32))
+    b = torch.from_numpy(rng.standard_normal(N).astype(np.float32))
+    assert echo.echo_linear_int8_workspace_bytes(M, N, K) == 0
+    wq, wsc = ref.quantize_tokens(x.float().cpu().numpy())
+    for ydt, kind, bias in ((torch.float32, echo.F32, None), (torch.bfloat16, echo.BF16, b)):
+        yb, y = matrix(M, N, N + pad, ydt, None, off)
+        echo.echo_linear_int8(x, K + pad, echo.BF16 if dt == "bf16" else echo.F32, w, K + pad, sw.to(DEV),
+                              None if bias is None else bias.to(DEV), M, N, K, y, N + pad, kind, None)
+        torch.cuda.synchronize()
+        want = torch.from_numpy(ref.gemm_int8(wq, wsc, wv.numpy(), sw.numpy(), None if bias is None else bias.numpy()))
+        same_bits(y, want.to(ydt))
+        untouched(yb, y)
+
+
+@pytest.mark.parametrize("H", [513, 1023, 1025, 2049, 3001, 4095, 4097, 5001, 6143, 8191, 8193, 16383])
+@pytest.mark.parametrize("x,r,h", [("bf16", "bf16", "bf16"), ("bf16", "f32", "bf16"), ("f32", "bf16", "f32"), ("f32", "f32", "f32"),
+                                   ("bf16", "f32", "f32"), ("f32", "f32", "bf16"), ("f32", "bf16", "bf16"), ("bf16", "bf16", "f32")])
+def test_rows_that_end_inside_a_chunk(echo, H, x, r, h):
+    """Each width's form, forward (also to 8 bits) and backward, with a last chunk that is not full."""
+    say("norm tail", H, x, r, h)
+    check_forward(echo, Case(9, H, x, r, "bf16", "i8", gate=4, pad=3, off=1))
+    check_forward(echo, Case(9, H, x, r, "f32", h, gate=4, beta=0.5))
+    check_backward(echo, Case(9, H, x, r, "f32", h, gate=4, beta=0.5, pad=3, off=1))
+    check_backward(echo, Case(14, H, x, r, "bf16", h, post=False))
+
+
+@pytest.mark.parametrize("H", [1024, 5001, 9000])
+def test_backward_far_rows(echo, H):
+    """Rows past 2^31 elements: the same bits as for rows next to one another."""
+    T, ld = 40, (1 << 31) // 39 + 8
+    say("backward far rows", H)
+    g = torch.Generator(device=DEV).manual_seed(H)
+    rnd = lambda *s: torch.randn(*s, generator=g, device=DEV)  # noqa: E731
+    v = rnd(4, T, H).bfloat16()
+    w_post, w_pre, gate = 1 + 0.2 * rnd(H), 1 + 0.2 * rnd(H), 0.5 + 0.3 * rnd(T, H)
+    ws = torch.empty(echo.echo_block_norm_backward_workspace_bytes(T, H), dtype=torch.uint8, device=DEV)
+    out = []
+    for dist in (H, ld):
+        x, r, dh, up = (matrix(T, H, dist, torch.bfloat16, t)[1] for t in v)
+        dx, dr = (matrix(T, H, dist, torch.bfloat16, None)[1] for _ in range(2))
+        dw = torch.full((2, H), 7.0, device=DEV)
+        dg = torch.full((T, H), 7.0, device=DEV)
+        a = echo.make_norm_args(x, r, w_post=w_post, w_pre=w_pre, gate=gate, gate_tokens=1)
+        echo.echo_block_norm_backward(a, echo.make_norm_grads(dh=dh, dr_out=up, dx=dx, dr=dr, dw_post=dw[0], dw_pre=dw[1], dgate=dg,
+                                                              workspace=ws))
+        torch.cuda.synchronize()
+        out.append([t.contiguous().cpu() for t in (dx, dr, dw, dg)])
+        del x, r, dh, up, dx, dr
+    for p, q in zip(*out):
+        same_bits(p, q)
