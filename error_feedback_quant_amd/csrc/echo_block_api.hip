@@ -524,7 +524,11 @@ int echo_linear_int8(const void* x, int64_t ldx, int x_dtype, const int8_t* w, i
 int echo_block_norm(const echo_norm_args* p, void* stream)
 {
     const int rc = check_norm(p, false);
-    if (rc || p->T == 0 || p->H == 0) return rc;
+    if (rc || p->T == 0) return rc;
+    if (p->H == 0) {        // tokens of no elements have the scales that quantizing them gives
+        if (p->h_dtype != ECHO_I8 || !p->h_scale) return ECHO_OK;
+        return echo_quantize_tokens(nullptr, 0, ECHO_F32, p->T, 0, nullptr, 0, p->h_scale, stream);
+    }
     const echo::NormArgs a = norm_args(*p);
     launch_block_norm(a, (hipStream_t)stream);
     return check_launch();

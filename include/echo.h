@@ -438,7 +438,8 @@ int echo_linear_int8(const void* x, int64_t ldx, int x_dtype, const int8_t* w, i
  * token, the sequence length one for each sequence, T or more one for all;
  * the last row may serve fewer.  r NULL is a stream of zeros (the first
  * norm of a model: post = 0, x the embeddings), w_post, w_pre and gate NULL
- * are ones, r_out or h may be NULL (not both).  r_out may be r.
+ * are ones, r_out or h may be NULL (not both).  r_out may be r.  H of 0 writes
+ * the scales of an 8-bit h (where h_scale is not NULL) and nothing else.
  * Constraints: T < 2^31, H <= 2^30 (ECHO_ESHAPE); eps > 0 and the scales
  * finite, w_post NULL where post = 0 (ECHO_EINVAL).
  */

@@ -313,3 +313,17 @@ def test_backward_far_rows(echo, H):
         del x, r, dh, up, dx, dr
     for p, q in zip(*out):
         same_bits(p, q)
+
+
+def test_no_columns_in_8_bits(echo):
+    """A token of no elements has the codes and the scale that quantizing it gives."""
+    say("norm without columns")
+    x = torch.empty(5, 0, device=DEV)
+    for wide in (0, 16):
+        s, want = (torch.full((6,), 7.0, device=DEV) for _ in range(2))
+        h = torch.empty(5, wide, dtype=torch.int8, device=DEV)
+        echo.echo_block_norm(echo.make_norm_args(x, h=h, h_scale=s[:5]))
+        echo.echo_quantize_tokens(x, 0, echo.F32, 5, 0, h, wide, want[:5])
+        torch.cuda.synchronize()
+        assert float(want[0]) != 7.0
+        same_bits(s, want)
