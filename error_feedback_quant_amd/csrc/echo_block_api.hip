@@ -114,13 +114,17 @@ void linear_fused_go(const echo::GemmI8Args& a, const void* x, hipStream_t st)
 
 // Tiles: one of the sizes below, by the estimated time of all rounds of tiles
 // over the CUs.  `us` is a full chip's round of that tile at K = 4096 as
-// measured, with direct loads and through registers; all grow alike with K.
+// measured, with direct loads and through registers.  A round also has a part
+// that K does not change (256 x 256: 15.2 us at K = 256, 18.6 at 512, 24.4 at
+// 1024, 61.9 at 4096), but the order of the tiles holds: of 17 sizes of 128 to
+// 8192 tokens at K = 256 to 4096 the choice is the fastest tile for 15 and 4
+// and 6 % behind for two; at 8192 x 8192 x 512 it took 87 us and 128 x 256 73.
 // The largest tile reads the least per product and wins where it fills the
-// chip (16384 x 4096 x 4096: 238 us, 270 with 128 x 256, 550 with 64 x 64);
+// chip (16384 x 4096 x 4096: 246 us, 276 with 128 x 256, 519 with 64 x 64);
 // small calls want a tile for every CU, whose loads come at about 30 bytes a
-// clock whatever the tile (100 x 4096 x 4096: 38 us with 256 x 256, 9.7 with
-// 64 x 64, 8.9 with 64 x 32).  Through registers the largest tile spills and
-// gains nothing over the next one (88 us each at 4096 x 4096 x 3584).
+// clock whatever the tile (100 x 4096 x 4096: 38 us with 256 x 256, 9.0 with
+// 64 x 64, 7.9 with 64 x 32).  Through registers the largest tile spilled and
+// gained nothing over the next one (4096 x 4096 x 3584).
 struct TileCost {
     int bm, bn;
     float us[2];
@@ -136,10 +140,12 @@ constexpr int64_t kCus = 256;
 void launch_gemm_i8(echo::GemmI8Args& a, hipStream_t st)
 {
     // Few tokens: the weight streams past them, without tiles, while the blocks
-    // of 16 channels are about as many as the CUs: 16 x 4096 x 4096 in 7.5 us
-    // (9.6 in 64 x 64 tiles), 32 in 9.4 (9.8); each block reads the tokens
-    // again, so past that only up to 8 of them (16 x 8192 x 8192: 18.4 and
-    // 15.5, 8 tokens 15.4 and 15.5).
+    // of 16 channels are about as many as the CUs.  Eight weights in turn, so
+    // that they come from memory: 1 x 4096 x 4096 in 6.5 us (7.5 in 64 x 32
+    // tiles), 8 tokens 7.3 (7.7), 16 8.1 (7.7), 32 9.9 (7.9); one weight that
+    // stays in cache: 5.1 (7.1), 5.7 (7.2), 6.4 (7.1), 8.4 (7.5).  Each block
+    // reads the tokens again, so with more channels only up to 8 of them (8 x
+    // 8192 x 8192: 17.3 and 18.8, 16 tokens 19.0 and 19.1).
     if ((a.M <= 8 || (a.M <= 32 && a.N <= 16 * kCus)) && grid_fits((a.N + 15) / 16, echo::kFewThreads)) {
         if (a.M <= 16) gemm_few_go<1, 0, 1, 1>(a, nullptr, st);
         else gemm_few_go<2, 0, 1, 1>(a, nullptr, st);

@@ -72,7 +72,9 @@ struct QuantTokArgs {
 
 // A token held in registers: G threads with C chunks of 8 elements each, one
 // pass over memory.  Bound by memory: 16384 x 4096 bf16 (201 MB) in 36 us, 5.6
-// TB/s (64, 128 or 512 threads a token: 37.7, 36.4, 38.3); 27 x 3584 in 2.3.
+// TB/s, with four inputs in turn (64, 128 or 512 threads a token: 37.7, 36.4,
+// 38.3), in 43 behind a product that has had the caches, in 30 with its input
+// still there; 27 x 3584 in 2.7.
 template <int G, int C, bool BF16, bool TAIL>
 __global__ __launch_bounds__(row_block<G>()) void quantize_tokens_kernel(const QuantTokArgs a)
 {
@@ -101,9 +103,11 @@ __global__ __launch_bounds__(row_block<G>()) void quantize_tokens_kernel(const Q
     }
 }
 
-// Tokens longer than a block's registers: one block per token, two passes.
+// Tokens longer than a block's registers: one block per token, two passes by
+// single elements (2048 x 20000 in bf16, 123 MB, takes 62 us).
 __global__ __launch_bounds__(kBlock) void quantize_long_tokens_kernel(const QuantTokArgs a)
-{    __shared__ uint32_t red[kBlock / 64];
+{
+    __shared__ uint32_t red[kBlock / 64];
     for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
         uint32_t m = 0;
         for (int k = threadIdx.x; k < a.K; k += kBlock) m = max(m, abs_bits(ld_elem(a.x, a.bf16, t * a.ldx + k)));
@@ -220,16 +224,17 @@ __global__ __launch_bounds__(kBlock) void gemm_i8_tile_kernel(const GemmI8Args a
 // the first fragments of the next stage are read under them; a barrier at the
 // stage's end would leave the matrix cores idle for an LDS round trip.
 //
-// Measured (direct loads): 4096 x 4096 x 3584 in 55 us (2.19 POP/s), 16384 x
-// 4096 x 4096 in 248 us (2.22 POP/s).  With 256 x 256 tiles the matrix cores
-// are busy for 64 % of a tile's cycles; a full chip then runs at about 1.8 GHz
+// Measured (direct loads): 4096 x 4096 x 3584 in 54 us (2.21 POP/s; 58 after a
+// while of full load), 16384 x 4096 x 4096 in 246 to 267 by the clock it gets,
+// 255 behind its quantization (2.16 POP/s).  With 256 x 256 tiles the matrix
+// cores are busy for 62 % of a tile's cycles; a full chip runs at about 1.8 GHz
 // (half of it at 2.4: 63 us for 256 tiles of K = 4096, 46 for 128), so beyond
 // that power bounds it: the 4-wave form of the tile, with a third less LDS
 // traffic but one wave on each SIMD, took 62 us.  Small tiles are bound by
 // their loads, which come at about 30 bytes a clock and CU whatever the tile;
 // splitting K over two halves of a block, or reading a whole stage's
 // fragments at once, made them no faster.  Rows at odd places need a fifth
-// word for each 16 bytes and more lines: 88 us at 4096 x 4096 x 3584.
+// word for each 16 bytes and more lines: 91 us at 4096 x 4096 x 3584.
 
 constexpr int kI8BK = 128;                   // bytes of K per stage
 constexpr int64_t kI8StageLd = int64_t(1) << 22;   // row distances below this keep a panel's offsets in 31 bits
@@ -557,9 +562,10 @@ void gemm_i8_stage_kernel(const GemmI8Args a)
 // bytes per instruction).  The eight partial sums meet in LDS; integer sums
 // are exact, so the split changes nothing.  Up to 16 MT tokens.
 //
-// Bound by the weight's way in: 1 x 4096 x 4096 takes 6.0 us, 2.8 TB/s over a
-// call with its launch, and 8 x 8192 x 8192 15.5 us, 4.3 TB/s, near what a
-// copy reaches.  All 64 KB that a CU has to read are asked for at once.
+// Bound by the weight's way in: with eight weights in turn 1 x 4096 x 4096 takes
+// 6.5 us, 2.6 TB/s over a call with its launch, and 8 x 8192 x 8192 17.3 us,
+// 3.9 TB/s; with one that stays in cache 5.1 and 15.3.  All 64 KB that a CU
+// has to read are asked for at once.
 //
 // XKIND 0 takes codes; 1 (bf16) and 2 (fp32) take up to FM tokens of
 // activations, held in registers in C chunks of 8 a thread, and every block
@@ -580,8 +586,8 @@ struct FewArgs {
 constexpr int few_pitch(int K) { return (K + 63) / 64 * 64 + 16; }
 
 // 16 codes on their way to registers.  SHIFT: the row may start between two
-// words; the words that hold the codes are loaded and shifted together (as
-// 16-byte loads at odd addresses: 14.4 us at 8 x 4096 x 4096, 6.7 aligned).
+// words; the words that hold the codes are loaded and shifted together (8 x
+// 4096 x 4096: 7.7 us, as 16-byte loads at odd addresses 14.4, aligned 5.7).
 template <bool SHIFT>
 struct Codes16 {
     u32x4 v;

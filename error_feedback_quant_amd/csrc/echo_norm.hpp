@@ -145,9 +145,9 @@ __device__ __forceinline__ void ld_branch8(const NormArgs& a, const void* gate, 
 // A token held in registers: G threads, C chunks of 8 elements each, every
 // byte moved once.  The weights stay in registers over the tokens of a group
 // of threads, and so does the gate while its row lasts.  Bound by memory:
-// 131072 x 1024 in bf16 (1.07 GB) takes 180 us, 5.95 TB/s (a device copy
+// 131072 x 1024 in bf16 (1.07 GB) takes 182 us, 5.9 TB/s (a device copy
 // reaches 4.9); 2048 x 4096 with an fp32 stream and gate (100 MB) 23 us; 64 x
-// 1024 is 4 us of load, two reductions and store after one another.
+// 1024 is 4.2 us of load, two reductions and store after one another.
 template <int G, int C, bool XB, bool RB, bool TAIL>
 __global__ __launch_bounds__(row_block<G>()) void block_norm_kernel(const NormArgs a)
 {
@@ -263,7 +263,8 @@ __device__ __forceinline__ float row_factor(const NormArgs& a, float* red, F val
 }
 
 // Rows too wide for registers: one block per token of any width, the row read
-// again in each pass (from L2 where it fits).
+// again in each pass (from L2 where it fits).  Single elements a lane and
+// load, so far from memory's rate: 2048 x 20000 in bf16 (328 MB) takes 355 us.
 __global__ __launch_bounds__(kBlock) void block_norm_any_kernel(const NormArgs a)
 {
     __shared__ float red[kBlock / 64];
@@ -322,7 +323,9 @@ __device__ __forceinline__ NormGrad norm_grad(const NormBwdArgs& b, int64_t t, i
 
 // Backward of rows too wide for registers (over 8192 elements), in passes that
 // read them again: each token's four numbers, the sums over tokens by columns,
-// then dx and dr.
+// then dx and dr.  Each pass loads single elements, so far from memory's rate:
+// 2048 x 12288 in bf16 (302 MB) takes 642 us, 3.3 ms with one gate row for all
+// tokens, where one thread walks a column.
 
 // the four numbers of a token that its gradients need
 __global__ __launch_bounds__(kBlock) void norm_bwd_stats_kernel(const NormBwdArgs b)
@@ -438,10 +441,10 @@ __global__ __launch_bounds__(kBlock) void norm_bwd_apply_kernel(const NormBwdArg
 // Three reductions a token: sum x^2; sum r'^2 with sum dh w_pre r'; and
 // sum dz w_post x.
 //
-// Bound by memory: 131072 x 1024 in bf16 (1.61 GB) takes 301 us, 5.35 TB/s,
+// Bound by memory: 131072 x 1024 in bf16 (1.61 GB) takes 303 us, 5.3 TB/s,
 // its second launch included.  One chunk a thread: with two the sums, weights
 // and two tokens' rows fill 256 registers and spill (333 to 341 us).  2048 x
-// 4096 with gate rows of 600 tokens (151 MB) takes 42 us, 36 + 4.4: one block
+// 4096 with gate rows of 600 tokens (151 MB) takes 42 us, 37 + 4.8: one block
 // of 8 waves on a CU, 8 tokens after one another, three barriers each.
 template <int G, int C, bool XB, bool RB, bool HB, bool TAIL>
 __global__ __launch_bounds__(row_block<G>()) void block_norm_bwd_kernel(const NormBwdArgs b)
@@ -764,7 +767,7 @@ __global__ __launch_bounds__(row_block<G>()) void block_norm_bwd_kernel(const No
     }
 }
 
-// Adds the partial sums (bound by latency: 4.4 to 6.6 us for 256 to 1024
+// Adds the partial sums (bound by latency: 3.9 to 6.1 us for 167 to 1024
 // partials): blockIdx.x a strip of 64 columns, blockIdx.y 0 and 1
 // dw_post and dw_pre, from 2 on the gate rows.  16 waves share a column's
 // partials and meet in LDS.
