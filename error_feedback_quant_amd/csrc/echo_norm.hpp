@@ -155,7 +155,7 @@ __global__ __launch_bounds__(row_block<G>()) void block_norm_kernel(const NormAr
     constexpr int kRows = row_block<G>() / G;
     const int g = threadIdx.x % G;
     int64_t t = (int64_t)blockIdx.x * kRows + threadIdx.x / G;
-    if constexpr (G == 64) t = __builtin_amdgcn_readfirstlane((int)t);
+    t = __builtin_amdgcn_readfirstlane((int)t);              // one row a wave at most: kept in scalar registers
     const int64_t step = (int64_t)gridDim.x * kRows;
     float w[C][8], w_pre[C][8];                              // w: beta gate w_post
     auto weights = [&](const void* gate, int64_t row) {
