@@ -27,7 +27,7 @@ HIP_FLAGS = [
 
 
 def sources():
-    return [os.path.join(CSRC, "echo_api.hip"), os.path.join(CSRC, "echo_block_api.hip")]
+    return [os.path.join(CSRC, f) for f in ("echo_api.hip", "echo_block_api.hip", "echo_int4_api.hip", "echo_cache_api.hip")]
 
 
 # test-only device code: the kernels' helpers evaluated on their own, built

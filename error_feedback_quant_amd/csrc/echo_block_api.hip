@@ -16,22 +16,15 @@
 namespace {
 
 using echo::aligned16;
+using echo::aligned_elem;
 using echo::aligned_to;
+using echo::bad_dim;
+using echo::bad_ld;
 using echo::check_launch;
-
-constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1;
-constexpr int64_t kMaxLd = int64_t(1) << 32;        // row strides; offsets are 64-bit
-constexpr int64_t kMaxGrid = int64_t(1) << 20;      // blocks of a launch; kernels stride over the rest
-
-bool float_dtype(int d) { return d == ECHO_F32 || d == ECHO_BF16; }
-size_t dtype_bytes(int d) { return d == ECHO_F32 ? 4 : (d == ECHO_BF16 ? 2 : 1); }
-bool aligned_elem(const void* p, int dtype) { return aligned_to(p, dtype_bytes(dtype)); }
-
-// rows of `cols` elements at a distance of ld (which a single row does not use)
-bool bad_ld(int64_t ld, int64_t rows, int64_t cols) { return rows > 1 && (ld < cols || ld > kMaxLd); }
-bool bad_dim(int64_t v, int64_t most) { return v < 0 || v > most; }
-
-unsigned grid_of(int64_t items) { return (unsigned)(items < kMaxGrid ? items : kMaxGrid); }
+using echo::float_dtype;
+using echo::grid_fits;
+using echo::grid_of;
+using echo::kMaxRows;
 
 template <int G, int C, bool BF16>
 void quantize_go(const echo::QuantTokArgs& a, hipStream_t st)
@@ -59,9 +52,6 @@ void launch_quantize(const echo::QuantTokArgs& a, hipStream_t st)
     if (a.bf16) quantize_sized<true>(a, st);
     else quantize_sized<false>(a, st);
 }
-
-// a launch's work-items are a 32-bit number
-bool grid_fits(int64_t blocks, int64_t threads) { return blocks * threads < (int64_t(1) << 32); }
 
 // NR 0: no form of this tile for rows that start anywhere
 template <int BM, int BN, int WM, int WN, int NS, int NR>

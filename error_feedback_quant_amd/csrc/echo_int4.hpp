@@ -1,0 +1,279 @@
+// echo_int4.hpp — gfx950 kernels of the linear layer with 4-bit weights: the
+// quantizer of a row's groups, and the product for few tokens.
+//
+// Product: y[m][n] = sum_g s[n][g] (sum_{k in g} x[m][k] q[n][k]
+//                                   - z[n][g] sum_{k in g} x[m][k]) + bias[n].
+// A code becomes the bfloat16 16 + q with two instructions for two of them
+// (shift and and-or: q goes to bits 3 .. 6 of the significand of 16.0), exact,
+// and the matrix cores sum x (16 + q) and, with a row of ones in place of the
+// weight, x itself; (16 + z) times the latter is taken off in fp32.  16 is the
+// least offset that a bfloat16 holds beside four bits: the sums cancel by a
+// factor of at most 31 / 15, where 128 + q would lose three bits more.
+#pragma once
+
+#include <type_traits>
+
+#include "echo_kernels.hpp"
+#include "echo_rows.hpp"
+
+namespace echo {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+// Reductions over L lanes (4, 8, 16 or 32, aligned): inside a 16-lane row by
+// DPP (the mirrors join halves whose lanes agree already), across two rows by
+// a swizzle.  All lanes of the group have to be active.
+template <int L, typename F>
+__device__ __forceinline__ uint32_t group_fold(uint32_t v, F f)
+{
+    v = f(v, (uint32_t)dpp_i<0xB1>((int)v));                 // quad_perm 1,0,3,2
+    v = f(v, (uint32_t)dpp_i<0x4E>((int)v));                 // quad_perm 2,3,0,1
+    if constexpr (L >= 8) v = f(v, (uint32_t)dpp_i<0x141>((int)v));    // row_half_mirror
+    if constexpr (L >= 16) v = f(v, (uint32_t)dpp_i<0x140>((int)v));   // row_mirror
+    if constexpr (L >= 32) v = f(v, (uint32_t)__builtin_amdgcn_ds_swizzle((int)v, 0x401F));   // lane ^ 16
+    return v;
+}
+template <int L>
+__device__ __forceinline__ uint32_t group_max_u32(uint32_t v)
+{
+    return group_fold<L>(v, [](uint32_t a, uint32_t b) { return max(a, b); });
+}
+
+// 4-bit codes of a lane's 8 elements and the parameter word of its group of L
+// lanes (the zero-aware quantizer; elements past the end are zeros, which its
+// range holds anyway).  top: the lane's largest |u| as bits.
+template <int L>
+__device__ __forceinline__ uint32_t quantize4(const float (&u)[8], uint32_t top, uint32_t& word)
+{
+    float lo, hi;
+    lane_stats<kZeroAware>(u, lo, hi);
+    // the patterns of zeros and negative floats order as unsigned integers by
+    // magnitude, those of zeros and positive floats as integers
+    const uint32_t l = group_max_u32<L>(__builtin_bit_cast(uint32_t, lo));
+    const uint32_t h = group_fold<L>(__builtin_bit_cast(uint32_t, hi),
+                                     [](uint32_t a, uint32_t b) { return (uint32_t)max((int)a, (int)b); });
+    const QParams p = make_params<4, kZeroAware>(__builtin_bit_cast(float, l), __builtin_bit_cast(float, h));
+    const bool bad = group_max_u32<L>(top) >= 0x7F800000u;
+    word = bad ? 0x7E00u : p.word;                           // NaN, zero point 0
+    uint32_t q = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) q |= (uint32_t)quant1<4, kZeroAware>(u[e], p) << (4 * e);
+    return bad ? 0u : q;
+}
+
+struct QuantGroupArgs {
+    const void* x;
+    uint8_t* q;
+    uint32_t* p;
+    int64_t ldx, ldq, ldp, T;
+    int K;
+    int shift;              // 1 << shift threads share a row (at least a group's, at most a block)
+};
+
+// A thread takes 8 elements, the L lanes of a group find its range together.
+// One pass over memory.
+template <int L, bool BF16>
+__global__ __launch_bounds__(kBlock) void quantize_groups_kernel(const QuantGroupArgs a)
+{
+    const int per = 1 << a.shift, rows = kBlock >> a.shift;
+    const int c0 = threadIdx.x & (per - 1), g = threadIdx.x & (L - 1);
+    const int chunks = (int)(((int64_t)a.K + 8 * L - 1) / (8 * L)) * L;      // whole groups
+    for (int64_t t0 = (int64_t)blockIdx.x * rows; t0 < a.T; t0 += (int64_t)gridDim.x * rows) {
+        const int64_t t = t0 + (threadIdx.x >> a.shift);
+        const bool in = t < a.T;
+        for (int c = c0 + per * (int)blockIdx.y; c < chunks; c += per * (int)gridDim.y) {
+            const int k = 8 * c;
+            const Raw8<BF16> raw = ld_raw8<BF16, true>(a.x, in ? t * a.ldx : 0, k, in ? a.K : 0);
+            float u[8];
+            uint32_t top = 0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                u[e] = raw_get(raw, e);
+                top = max(top, abs_bits(u[e]));
+            }
+            uint32_t word;
+            uint32_t q = quantize4<L>(u, top, word);
+            if (!in || k >= a.K) continue;
+            uint8_t* to = a.q + t * a.ldq + 4 * (int64_t)c;
+            if (k + 8 <= a.K) {
+                __builtin_memcpy(to, &q, 4);
+            } else {
+                const int n = a.K - k;                       // 1 .. 7
+                q &= (1u << (4 * n)) - 1u;
+                for (int i = 0; i < (n + 1) / 2; ++i) to[i] = (uint8_t)(q >> (8 * i));
+            }
+            if (g == 0) a.p[t * a.ldp + c / L] = word;
+        }
+    }
+}
+
+// ------------------------------------------------------------- few tokens --
+//
+// A block of 8 waves takes 16 channels and 16 MT tokens; its waves take every
+// eighth unit of K (128 elements, or a group of 256) and their sums meet in
+// LDS in a fixed order.  A lane's load of up to 16 bytes is its operand of the
+// next MFMAs: it holds 8 W consecutive codes of its row, W from 1 to 4, and
+// the fragments of x take the same order of k, which a sum does not see.
+
+constexpr int kInt4Waves = 8;
+constexpr int kInt4Threads = 64 * kInt4Waves;
+
+struct Int4Args {
+    const void* x;
+    const uint8_t* w;
+    const uint32_t* p;
+    const float* bias;
+    void* y;
+    int64_t M, N, ldx, ldw, ldp, ldy;
+    int K;
+    int bf16;               // of y
+};
+
+// codes 2i and 2i + 8 .. : the pairs (0, 4), (1, 5), (2, 6), (3, 7) of a word's
+// nibbles as bfloat16 16 + q
+__device__ __forceinline__ bf16x8 codes_bf16(uint32_t w)
+{
+    u32x4 r;
+    r.x = ((w << 3) & 0x00780078u) | 0x41804180u;
+    r.y = ((w >> 1) & 0x00780078u) | 0x41804180u;
+    r.z = ((w >> 5) & 0x00780078u) | 0x41804180u;
+    r.w = ((w >> 9) & 0x00780078u) | 0x41804180u;
+    return __builtin_bit_cast(bf16x8, r);
+}
+
+// two floats' upper halves as a pair
+__device__ __forceinline__ uint32_t upper_pair(float lo, float hi)
+{
+    return __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, hi), __builtin_bit_cast(uint32_t, lo), 0x07060302u);
+}
+
+// x's 8 elements in the order of codes_bf16, as P bfloat16 parts that sum to
+// them: one for bf16, three (8 + 8 + 8 bits) for fp32.  Truncation makes each
+// part, so each rest is exact.
+template <bool BF16, int P>
+__device__ __forceinline__ void x_parts(const Raw8<BF16>& r, bf16x8 (&f)[P])
+{
+    if constexpr (BF16) {
+        u32x4 o;
+        o.x = __builtin_amdgcn_perm(r.v[0].z, r.v[0].x, 0x05040100u);
+        o.y = __builtin_amdgcn_perm(r.v[0].z, r.v[0].x, 0x07060302u);
+        o.z = __builtin_amdgcn_perm(r.v[0].w, r.v[0].y, 0x05040100u);
+        o.w = __builtin_amdgcn_perm(r.v[0].w, r.v[0].y, 0x07060302u);
+        f[0] = __builtin_bit_cast(bf16x8, o);
+    } else {
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = raw_get(r, i);
+            v[2 * i + 1] = raw_get(r, i + 4);
+        }
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            u32x4 o;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                o[i] = upper_pair(v[2 * i], v[2 * i + 1]);
+                v[2 * i] -= __builtin_bit_cast(float, o[i] << 16);
+                v[2 * i + 1] -= __builtin_bit_cast(float, o[i] & 0xFFFF0000u);
+            }
+            f[p] = __builtin_bit_cast(bf16x8, o);
+        }
+    }
+}
+
+// BYTES (4, 8 or 16) of codes from byte `at` of a row of `bytes`, zeros past
+// its end
+template <int BYTES>
+__device__ __forceinline__ u32x4 ld_codes4(const uint8_t* row, int64_t at, int64_t bytes)
+{
+    u32x4 v = {0, 0, 0, 0};
+    if (at + BYTES <= bytes) {
+        __builtin_memcpy(&v, row + at, BYTES);
+    } else {
+        for (int i = 0; i < BYTES && at + i < bytes; ++i) v[i / 4] |= (uint32_t)row[at + i] << (8 * (i & 3));
+    }
+    return v;
+}
+
+template <int GROUP, int MT, bool BF16>
+__global__ __launch_bounds__(kInt4Threads) void linear_int4_kernel(const Int4Args a)
+{
+    constexpr int kPart = BF16 ? 1 : 3;
+    constexpr int kSub = GROUP < 128 ? GROUP : 128;          // elements of K that one load of each lane covers
+    constexpr int W = kSub / 32;                             // words of a lane's load
+    constexpr int kUnit = GROUP < 128 ? 128 : GROUP;
+    __shared__ f32x4 part[kInt4Waves][MT][64];
+    const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const uint32_t col = lane & 15u, g = lane >> 4;
+    const int64_t n0 = (int64_t)blockIdx.x * 16, m0 = (int64_t)blockIdx.y * (16 * MT);
+    const uint8_t* wr = a.w + min(n0 + col, a.N - 1) * a.ldw;
+    const int64_t bytes = ((int64_t)a.K + 1) / 2;
+    const uint32_t* pr[4];
+#pragma unroll
+    for (int v = 0; v < 4; ++v) pr[v] = a.p + min(n0 + 4 * g + v, a.N - 1) * a.ldp;
+    int64_t xr[MT];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) xr[t] = min(m0 + 16 * t + col, a.M - 1) * a.ldx;
+    const u32x4 one4 = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+    const bf16x8 ones = __builtin_bit_cast(bf16x8, one4);
+
+    f32x4 y[MT];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) y[t] = f32x4{0, 0, 0, 0};
+    const int units = (int)(((int64_t)a.K + kUnit - 1) / kUnit);
+    for (int u = wave; u < units; u += kInt4Waves) {
+        f32x4 acc[MT], xs[MT];
+#pragma unroll
+        for (int s = 0; s < kUnit / kSub; ++s) {
+            const int k0 = u * kUnit + s * kSub;
+            if (s % (GROUP / kSub) == 0) {
+#pragma unroll
+                for (int t = 0; t < MT; ++t) acc[t] = xs[t] = f32x4{0, 0, 0, 0};
+            }
+            const int kl = k0 + 8 * W * (int)g;              // of this lane
+            const u32x4 w = ld_codes4<4 * W>(wr, kl / 2, bytes);
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+                const bf16x8 fw = codes_bf16(w[i]);
+#pragma unroll
+                for (int t = 0; t < MT; ++t) {
+                    bf16x8 fx[kPart];
+                    x_parts<BF16, kPart>(ld_raw8<BF16, true>(a.x, xr[t], kl + 8 * i, a.K), fx);
+#pragma unroll
+                    for (int p = 0; p < kPart; ++p) {
+                        acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fw, fx[p], acc[t], 0, 0, 0);
+                        xs[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, fx[p], xs[t], 0, 0, 0);
+                    }
+                }
+            }
+            if ((s + 1) % (GROUP / kSub) == 0 && k0 / GROUP * GROUP < a.K) {
+                const int grp = k0 / GROUP;
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    const uint32_t word = pr[v][grp];
+                    const float sc = half_lo(word), z = half_hi(word) + 16.0f;
+#pragma unroll
+                    for (int t = 0; t < MT; ++t)
+                        y[t][v] = __builtin_fmaf(sc, __builtin_fmaf(-z, xs[t][v], acc[t][v]), y[t][v]);
+                }
+            }
+        }
+    }
+    // lane l of tile t holds channels 4 (l / 16) .. + 3 of token 16 t + l % 16
+#pragma unroll
+    for (int t = 0; t < MT; ++t) part[wave][t][lane] = y[t];
+    __syncthreads();
+    for (uint32_t i = tid; i < 64 * MT; i += kInt4Threads) {
+        f32x4 s = part[0][i >> 6][i & 63u];
+#pragma unroll
+        for (int w = 1; w < kInt4Waves; ++w) s += part[w][i >> 6][i & 63u];
+        const int64_t m = m0 + 16 * (i >> 6) + (i & 15u);
+        const int64_t n = n0 + 4 * ((i & 63u) >> 4);
+        if (m >= a.M) continue;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (n + e < a.N) st_elem(a.y, a.bf16, m * a.ldy + n + e, a.bias ? s[e] + a.bias[n + e] : s[e]);
+    }
+}
+
+}  // namespace echo

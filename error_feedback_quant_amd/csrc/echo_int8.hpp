@@ -24,29 +24,9 @@
 namespace echo {
 
 constexpr int kI8MaxK = (1 << 17) - 1;       // 2^14 * K stays below 2^31
-constexpr float kI8Tiny = 0x1p-100f;         // smallest token magnitude that sets a scale
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x16 __attribute__((ext_vector_type(16)));
-
-// max of |x| by bit pattern: the patterns of non-negative floats order as
-// unsigned integers, with NaN above infinity above every finite value
-__device__ __forceinline__ uint32_t abs_bits(float x) { return __builtin_bit_cast(uint32_t, x) & 0x7FFFFFFFu; }
-
-struct TokenScale {
-    float scale, inv;
-};
-__device__ __forceinline__ TokenScale token_scale(uint32_t amax_bits)
-{
-    if (amax_bits >= 0x7F800000u) return {__builtin_bit_cast(float, 0x7FC00000u), 0.0f};
-    const float a = fmaxf(__builtin_bit_cast(float, amax_bits), kI8Tiny);
-    return {a / 127.0f, 127.0f / a};
-}
-// code of x under a token's inv; inv == 0 marks a token without one
-__device__ __forceinline__ int token_code(float x, float inv)
-{
-    return inv == 0.0f ? 0 : (int)__builtin_rintf(x * inv);
-}
 
 // Largest value over the block; every thread gets it.  red: one word per wave.
 __device__ __forceinline__ uint32_t block_max_u32(uint32_t v, uint32_t* red)

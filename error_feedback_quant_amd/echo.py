@@ -29,7 +29,7 @@ _lib = ctypes.CDLL(LIB_PATH)
 
 OK, EINVAL, EALIGN, EUNSUP, ESHAPE, EHIP, ETOOBIG = 0, -1, -2, -3, -4, -5, -6
 OUT_F32, OUT_BF16 = 0, 1
-F32, BF16, I8 = 0, 1, 2
+F32, BF16, I8, I4 = 0, 1, 2, 3
 ERR_NEGATED = 1
 QUANT_NAIVE, QUANT_SYMMETRIC = 2, 4
 X_ALL = 8
@@ -83,6 +83,35 @@ class NormGrads(Structure):
     ]
 
 
+class Cache(Structure):
+    """Mirror of echo_cache."""
+    _fields_ = [
+        ("pages", c_int64), ("page_tokens", c_int64), ("heads", c_int64), ("width", c_int64),
+        ("ld_page", c_int64), ("ld_head", c_int64), ("ld_token", c_int64),
+        ("ld_scale_page", c_int64), ("ld_scale_head", c_int64),
+        ("kind", c_int), ("k", c_void_p), ("v", c_void_p), ("k_scale", c_void_p), ("v_scale", c_void_p),
+    ]
+
+
+class Seqs(Structure):
+    """Mirror of echo_seqs."""
+    _fields_ = [
+        ("seqs", c_int64), ("tokens", c_int64), ("table_pages", c_int64), ("ld_table", c_int64),
+        ("max_new", c_int64), ("max_len", c_int64),
+        ("starts", c_void_p), ("lens", c_void_p), ("page_table", c_void_p),
+    ]
+
+
+class AttentionArgs(Structure):
+    """Mirror of echo_attention_args."""
+    _fields_ = [
+        ("cache", Cache), ("seqs", Seqs),
+        ("q_heads", c_int64), ("ld_q", c_int64), ("ld_out", c_int64), ("window", c_int64),
+        ("causal", c_int), ("scale", c_float),
+        ("q", c_void_p), ("out", c_void_p), ("lse", c_void_p),
+    ]
+
+
 _lib.echo_status_str.restype = c_char_p
 _lib.echo_status_str.argtypes = [c_int]
 _lib.echo_last_hip_error.restype = c_int
@@ -125,6 +154,21 @@ _lib.echo_block_norm_backward_workspace_bytes.restype = c_size_t
 _lib.echo_block_norm_backward_workspace_bytes.argtypes = [c_int64, c_int64]
 _lib.echo_block_norm_backward.restype = c_int
 _lib.echo_block_norm_backward.argtypes = [POINTER(NormArgs), POINTER(NormGrads), c_void_p]
+_lib.echo_quantize_groups.restype = c_int
+_lib.echo_quantize_groups.argtypes = [c_void_p, c_int64, c_int, c_int64, c_int64, c_int, c_void_p, c_int64, c_void_p, c_int64,
+                                      c_void_p]
+_lib.echo_linear_int4_workspace_bytes.restype = c_size_t
+_lib.echo_linear_int4_workspace_bytes.argtypes = [c_int64, c_int64, c_int64, c_int]
+_lib.echo_linear_int4.restype = c_int
+_lib.echo_linear_int4.argtypes = [c_void_p, c_int64, c_int, c_void_p, c_int64, c_void_p, c_int64, c_int, c_void_p, c_int64,
+                                  c_int64, c_int64, c_void_p, c_int64, c_int, c_void_p, c_size_t, c_void_p]
+for _f in (_lib.echo_cache_write, _lib.echo_cache_read):
+    _f.restype = c_int
+    _f.argtypes = [POINTER(Cache), POINTER(Seqs), c_void_p, c_int64, c_void_p, c_int64, c_int, c_void_p]
+_lib.echo_cache_attention_workspace_bytes.restype = c_size_t
+_lib.echo_cache_attention_workspace_bytes.argtypes = [POINTER(AttentionArgs)]
+_lib.echo_cache_attention.restype = c_int
+_lib.echo_cache_attention.argtypes = [POINTER(AttentionArgs), c_void_p, c_size_t, c_void_p]
 
 
 def lib():
@@ -394,3 +438,125 @@ def echo_block_norm_backward(args: NormArgs, grads: NormGrads, stream=None):
         raise ValueError("the gradients' shapes or types do not fit the forward call's arguments")
     _check("echo_block_norm_backward", _lib.echo_block_norm_backward(
         ctypes.byref(args), ctypes.byref(grads), _stream(stream)))
+
+
+# -------------------------------------------------------- serving operators --
+
+def _bytes(workspace, workspace_bytes):
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    return workspace_bytes
+
+
+def echo_quantize_groups(x, ldx, x_dtype, T, K, group, codes, ldq, params, ldp, stream=None):
+    """params holds (scale, zero point) pairs of binary16, ldp counts pairs."""
+    _check("echo_quantize_groups", _lib.echo_quantize_groups(
+        _ptr(x), ldx, x_dtype, T, K, group, _ptr(codes), ldq, _ptr(params), ldp, _stream(stream)))
+
+
+def echo_linear_int4_workspace_bytes(M, N, K, group) -> int:
+    return int(_lib.echo_linear_int4_workspace_bytes(M, N, K, group))
+
+
+def echo_linear_int4(x, ldx, x_dtype, w, ldw, params, ldp, group, bias, M, N, K, y, ldy, y_dtype, workspace=None,
+                     workspace_bytes=None, stream=None):
+    _check("echo_linear_int4", _lib.echo_linear_int4(
+        _ptr(x), ldx, x_dtype, _ptr(w), ldw, _ptr(params), ldp, group, _ptr(bias), M, N, K, _ptr(y), ldy, y_dtype,
+        _ptr(workspace), _bytes(workspace, workspace_bytes), _stream(stream)))
+
+
+_CACHE_KINDS = {torch.bfloat16: BF16, torch.int8: I8, torch.uint8: I4}
+
+
+def make_cache(k, v, k_scale=None, v_scale=None):
+    """Fill an echo_cache from tensors: k and v [pages, heads, page_tokens,
+    width] of bfloat16, int8 or (4 bits, two to a byte: the last dimension is
+    width / 2) uint8, in any order of memory that keeps a token's row together;
+    k_scale and v_scale [pages, heads, page_tokens] of float32 for int8, with a
+    last dimension of 2 of float16 (scale, zero point) for uint8.  It keeps the
+    tensors alive and can be used again."""
+    kind = _CACHE_KINDS.get(k.dtype)
+    if kind is None or k.dim() != 4 or v.shape != k.shape or v.dtype != k.dtype or v.stride() != k.stride() or k.stride(3) != 1:
+        raise ValueError(f"k and v: {tuple(k.shape)} {k.dtype} strides {k.stride()} and {tuple(v.shape)} {v.dtype} strides "
+                         f"{v.stride()}, expected one shape, type and order of bfloat16, int8 or uint8 with rows together")
+    pages, heads, page_tokens, width = k.shape
+    each = 2 if kind == I4 else 1
+    ld = [d * each for d in k.stride()[:3]]
+    sp = sh = 0
+    if kind == BF16:
+        if k_scale is not None or v_scale is not None:
+            raise ValueError("a bfloat16 cache has no scales")
+    else:
+        shape, dtype = ((pages, heads, page_tokens), torch.float32) if kind == I8 else ((pages, heads, page_tokens, 2), torch.float16)
+        for t in (k_scale, v_scale):
+            if t is None or t.shape != shape or t.dtype != dtype or t.stride() != k_scale.stride():
+                raise ValueError(f"scales: expected two of {shape} {dtype} in one order")
+        st = k_scale.stride()
+        if st[2] != each and page_tokens > 1 or kind == I4 and st[3] != 1 or st[0] % each or st[1] % each:
+            raise ValueError(f"scales: strides {st}, expected those of a head's tokens of a page together")
+        sp, sh = st[0] // each, st[1] // each
+    c = Cache(pages, page_tokens, heads, width * each, *ld, sp, sh, kind, k.data_ptr(), v.data_ptr(), _ptr(k_scale), _ptr(v_scale))
+    c.keep = (k, v, k_scale, v_scale)
+    return c
+
+
+def _int32(t, shape, what):
+    if t.shape != shape or t.dtype != torch.int32 or (t.stride(-1) != 1 and shape[-1] > 1):
+        raise ValueError(f"{what}: {tuple(t.shape)} {t.dtype} strides {t.stride()}, expected {tuple(shape)} of int32")
+    return t.data_ptr()
+
+
+def make_seqs(starts, lens, page_table, tokens, max_new=None, max_len=None):
+    """Fill an echo_seqs from int32 tensors: starts [seqs + 1], lens [seqs],
+    page_table [seqs, table_pages].  max_new and max_len only decide how work
+    is split; None: any number of the tokens, as long as the table holds.  It
+    keeps the tensors alive and can be used again."""
+    n = lens.shape[0]
+    pages = page_table.shape[1]
+    s = Seqs(n, tokens, pages, page_table.stride(0), tokens if max_new is None else max_new,
+             (1 << 62) if max_len is None else max_len, _int32(starts, (n + 1,), "starts"), _int32(lens, (n,), "lens"),
+             _int32(page_table, (n, pages), "page_table"))
+    s.keep = (starts, lens, page_table)
+    return s
+
+
+def _new_rows(k, v, cache, seqs):
+    shape = (seqs.tokens, cache.heads * cache.width)
+    pk, ld_k, kind = _rows(k, shape, "k", _FLOATS)
+    pv, ld_v, _ = _rows(v, shape, "v", (kind,))
+    return pk, ld_k, pv, ld_v, kind
+
+
+def echo_cache_write(cache: Cache, seqs: Seqs, k, v, stream=None):
+    """k and v: [tokens, heads * width], float32 or bfloat16, in contiguous rows."""
+    _check("echo_cache_write", _lib.echo_cache_write(
+        ctypes.byref(cache), ctypes.byref(seqs), *_new_rows(k, v, cache, seqs), _stream(stream)))
+
+
+def echo_cache_read(cache: Cache, seqs: Seqs, k, v, stream=None):
+    _check("echo_cache_read", _lib.echo_cache_read(
+        ctypes.byref(cache), ctypes.byref(seqs), *_new_rows(k, v, cache, seqs), _stream(stream)))
+
+
+def make_attention_args(cache: Cache, seqs: Seqs, q, out, heads, lse=None, scale=None, causal=True, window=0):
+    """Fill an echo_attention_args: q and out [tokens, heads * width] of
+    bfloat16 in contiguous rows, lse float32 [tokens, heads]; scale None is
+    width ** -0.5.  It keeps all tensors alive and can be used again."""
+    shape = (seqs.tokens, heads * cache.width)
+    pq, ld_q, _ = _rows(q, shape, "q", (BF16,))
+    po, ld_o, _ = _rows(out, shape, "out", (BF16,))
+    if lse is not None and (lse.shape != (seqs.tokens, heads) or lse.dtype != torch.float32 or not lse.is_contiguous()):
+        _refuse(lse, (seqs.tokens, heads), "lse", (F32,))
+    a = AttentionArgs(cache, seqs, heads, ld_q, ld_o, window, 1 if causal else 0,
+                      cache.width ** -0.5 if scale is None else scale, pq, po, _ptr(lse))
+    a.keep = (cache, seqs, q, out, lse)
+    return a
+
+
+def echo_cache_attention_workspace_bytes(args: AttentionArgs) -> int:
+    return int(_lib.echo_cache_attention_workspace_bytes(ctypes.byref(args)))
+
+
+def echo_cache_attention(args: AttentionArgs, workspace=None, workspace_bytes=None, stream=None):
+    _check("echo_cache_attention", _lib.echo_cache_attention(
+        ctypes.byref(args), _ptr(workspace), _bytes(workspace, workspace_bytes), _stream(stream)))

@@ -75,7 +75,7 @@ enum echo_status {
 enum echo_out_dtype { ECHO_OUT_F32 = 0, ECHO_OUT_BF16 = 1 };
 
 /* element types of the block operators (same values as echo_out_dtype) */
-enum echo_dtype { ECHO_F32 = 0, ECHO_BF16 = 1, ECHO_I8 = 2 };
+enum echo_dtype { ECHO_F32 = 0, ECHO_BF16 = 1, ECHO_I8 = 2, ECHO_I4 = 3 };
 
 /* flags for echo_quantize_ef / echo_reduce_segment / echo_gemm_quantize_ef
  * (and echo_sim_args.quant for the two quantizer bits) */
@@ -498,6 +498,176 @@ typedef struct echo_norm_grads {
 
 size_t echo_block_norm_backward_workspace_bytes(int64_t T, int64_t H);
 int echo_block_norm_backward(const echo_norm_args* args, const echo_norm_grads* grads, void* stream);
+
+/*
+ * Serving operators: a rank's step between the norm's output and the message
+ * of the all-reduce with low-bit weights and a low-bit cache.  Conventions of
+ * the block operators, and:
+ *  - 4-bit codes lie two to a byte, the even element in the low nibble; a
+ *    value is (q - z) * s with its group's echo_qparam, as everywhere above.
+ *  - 4-bit codes and parameters are made by the full method's quantizer
+ *    (echo_quantize_ef), bit for bit.  A group that holds an infinity or a NaN
+ *    gets the scale NaN, the zero point 0 and codes 0.
+ */
+
+/*
+ * echo_quantize_groups — 4-bit codes and parameters of every `group`
+ * consecutive elements of a row; the last group of a row may be shorter.
+ *
+ *   x (device, in)       [T][K], ECHO_F32 or ECHO_BF16, rows at ldx
+ *   codes (device, out)  [T][(K + 1) / 2] bytes, rows at ldq bytes; the high
+ *                        nibble behind an odd K is 0
+ *   params (device, out) [T][ceil(K / group)], rows at ldp, 4-byte aligned
+ * Constraints: group 32, 64, 128 or 256 (ECHO_EUNSUP); 0 <= K <= 2^30,
+ * 0 <= T < 2^31 (ECHO_ESHAPE).
+ */
+int echo_quantize_groups(const void* x, int64_t ldx, int x_dtype, int64_t T, int64_t K, int group, uint8_t* codes,
+                         int64_t ldq, echo_qparam* params, int64_t ldp, void* stream);
+
+/*
+ * echo_linear_int4 — a linear layer with 4-bit weights, for few tokens:
+ *   y[m][n] = sum_g s[n][g] * sum_{k in g} x[m][k] * (q[n][k] - z[n][g])  (+ bias[n])
+ * The products are exact and summed in fp32, group by group; a group's sum
+ * takes its scale in fp32, and a bf16 y is rounded once.  The order of the
+ * sums is fixed: equal calls give equal bits.  z is an integer from 0 to 15
+ * (what the quantizer above makes); other zero points round in z + 16.
+ * A token that holds an infinity or a NaN is NaN throughout.  It is made for
+ * few tokens: every 64 tokens read the weight again.
+ *
+ *   x (device, in)      [M][K], ECHO_F32 or ECHO_BF16, rows at ldx
+ *   w (device, in)      [N][(K + 1) / 2] bytes of codes, rows at ldw bytes
+ *   params (device, in) [N][ceil(K / group)], rows at ldp
+ *   bias (device, in)   fp32 [N] or NULL
+ *   y (device, out)     [M][N], ECHO_F32 or ECHO_BF16, rows at ldy
+ * Constraints: group as above; 0 <= K <= 2^30, M and N < 2^31 and at most
+ * 2^23 tiles of 16 channels by 64 tokens (ECHO_ESHAPE).  M or N of 0 enqueues
+ * nothing; K of 0 gives y = bias (or 0).  The workspace (device, 16-byte
+ * aligned, at least echo_linear_int4_workspace_bytes) may be NULL where that
+ * function returns 0.
+ */
+size_t echo_linear_int4_workspace_bytes(int64_t M, int64_t N, int64_t K, int group);
+int echo_linear_int4(const void* x, int64_t ldx, int x_dtype, const uint8_t* w, int64_t ldw, const echo_qparam* params,
+                     int64_t ldp, int group, const float* bias, int64_t M, int64_t N, int64_t K, void* y, int64_t ldy,
+                     int y_dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * echo_cache — a paged cache of keys and values: `pages` pages of
+ * `page_tokens` tokens, each token a row of `width` elements for each of
+ * `heads` heads.  Element d of head h of the token in slot i of page p lies at
+ *   p * ld_page + h * ld_head + i * ld_token + d
+ * in k and in v (in elements; rows do not overlap).  Rows are
+ *   ECHO_BF16  the values
+ *   ECHO_I8    codes with an fp32 scale a row: those of echo_quantize_tokens
+ *   ECHO_I4    codes with an echo_qparam a row: those of echo_quantize_groups
+ *              with the row as its group
+ * and a row's scale or parameter lies at p * ld_scale_page + h * ld_scale_head
+ * + i in k_scale and v_scale (NULL for ECHO_BF16).
+ * Constraints: kind one of the three (ECHO_EUNSUP); width a multiple of 8 from
+ * 8 to 256, the three ld multiples of 8, page_tokens >= 1, pages and
+ * page_tokens < 2^31, heads <= 65535 (ECHO_ESHAPE); k and v 16-byte, the
+ * scales 4-byte aligned.
+ */
+typedef struct echo_cache {
+    int64_t pages, page_tokens, heads, width;
+    int64_t ld_page, ld_head, ld_token;            /* distances in elements of k and v */
+    int64_t ld_scale_page, ld_scale_head;          /* distances in entries of k_scale and v_scale */
+    int kind;                                      /* ECHO_BF16, ECHO_I8 or ECHO_I4 */
+    void* k;
+    void* v;
+    void* k_scale;                                 /* float or echo_qparam */
+    void* v_scale;
+} echo_cache;
+
+/*
+ * echo_seqs — the sequences of a call.  `tokens` rows (of new keys and values,
+ * of queries, of outputs) belong to `seqs` sequences, one after the other:
+ * sequence b has rows starts[b] .. starts[b + 1] - 1, the last ones of its
+ * lens[b] tokens.  So row starts[b] + i stands at position
+ *   lens[b] - (starts[b + 1] - starts[b]) + i
+ * and the token at position t is in slot t % page_tokens of page
+ * page_table[b * ld_table + t / page_tokens].
+ *
+ * These arrays are read on the device and cannot be checked by the host.  The
+ * kernels read and write nothing outside the buffers whatever they hold: a
+ * token has no place where its position is negative or its entry of the table
+ * is past table_pages or names no page.  A sequence whose rows are not all
+ * among 0 .. tokens - 1 is not taken; rows of no sequence are left as they were.
+ * max_new and max_len (the most rows and the greatest length of a sequence)
+ * decide how work is split.  Results are right, but slower, where they are
+ * too small or too large.
+ * Constraints: seqs, tokens, table_pages < 2^31, max_new and max_len >= 0
+ * (ECHO_ESHAPE); int32 arrays 4-byte aligned.  No sequences or no tokens
+ * enqueue nothing.
+ */
+typedef struct echo_seqs {
+    int64_t seqs, tokens, table_pages, ld_table;
+    int64_t max_new, max_len;
+    const int32_t* starts;                         /* (device) [seqs + 1], from 0, not decreasing */
+    const int32_t* lens;                           /* (device) [seqs] */
+    const int32_t* page_table;                     /* (device) [seqs][table_pages], rows at ld_table */
+} echo_seqs;
+
+/*
+ * echo_cache_write — the new tokens' keys and values, quantized on their way
+ * into the cache.  Tokens without a place are left out; no two may have the
+ * same.  Slots of other tokens are not touched.
+ *   k, v (device, in)  [tokens][heads * width], ECHO_F32 or ECHO_BF16 (rounded
+ *                      once into an ECHO_BF16 cache), rows at ld_k and ld_v
+ * Constraints: tokens * heads < 2^31 (ECHO_ESHAPE).
+ */
+int echo_cache_write(const echo_cache* cache, const echo_seqs* seqs, const void* k, int64_t ld_k, const void* v,
+                     int64_t ld_v, int dtype, void* stream);
+
+/*
+ * echo_cache_read — the same tokens back from the cache as values, (q - z) * s
+ * in fp32, rounded once to bf16 where k and v are bf16.  Tokens without a
+ * place give NaN.  With starts the sums of lens it reads whole sequences.
+ *   k, v (device, out)  [tokens][heads * width], ECHO_F32 or ECHO_BF16
+ */
+int echo_cache_read(const echo_cache* cache, const echo_seqs* seqs, void* k, int64_t ld_k, void* v, int64_t ld_v,
+                    int dtype, void* stream);
+
+/*
+ * echo_cache_attention — attention of the new tokens over the cache, in which
+ * their own keys and values are already (echo_cache_write):
+ *   x_j = scale * sum_d q[d] * k_j[d],  m = max_j x_j,  p_j = exp(x_j - m)
+ *   out = sum_j p_j * v_j / sum_j p_j,  lse = m + log sum_j p_j
+ * over the tokens j that the row sees: 0 <= j <= position (causal = 1) or
+ * 0 <= j < lens (causal = 0), and j > position - window where window > 0.  A
+ * row that sees nothing gives 0 and an lse of -infinity.  Query head h reads
+ * head h / (q_heads / heads) of the cache.
+ * Scores, maxima, sums and outputs are held in fp32.  The weights p_j (times
+ * v's scale) are rounded to bf16 for the product with v; products with codes
+ * are exact.  Equal calls give equal bits.
+ * A row is NaN where its scores leave fp32, where its q holds an infinity or a
+ * NaN, where it sees a token that has no place, and where it sees a token
+ * whose key or value holds one (there at least in the elements that the
+ * formulas make so); tokens that a row does not see never touch it.
+ *
+ *   q (device, in)     bfloat16 bits [tokens][q_heads * width], rows at ld_q
+ *   out (device, out)  bfloat16 bits [tokens][q_heads * width], rows at ld_out
+ *   lse (device, out)  fp32 [tokens][q_heads], or NULL
+ * Constraints: q_heads a multiple of heads (ECHO_ESHAPE), tokens * q_heads <
+ * 2^31 (ECHO_ESHAPE), scale finite, window >= 0, causal 0 or 1 (ECHO_EINVAL).
+ * The workspace (device, 16-byte aligned, at least
+ * echo_cache_attention_workspace_bytes of the same arguments) holds what the
+ * parts of a long sequence leave to be joined; it may be NULL where that
+ * function returns 0.  Calls that may overlap in time need one each.
+ */
+typedef struct echo_attention_args {
+    echo_cache cache;
+    echo_seqs seqs;
+    int64_t q_heads, ld_q, ld_out;
+    int64_t window;                                /* tokens a row sees at most, 0 for all */
+    int causal;
+    float scale;
+    const uint16_t* q;
+    uint16_t* out;
+    float* lse;
+} echo_attention_args;
+
+size_t echo_cache_attention_workspace_bytes(const echo_attention_args* args);
+int echo_cache_attention(const echo_attention_args* args, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Static description of a status code. */
 const char* echo_status_str(int status);
