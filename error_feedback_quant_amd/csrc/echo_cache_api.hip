@@ -3,6 +3,7 @@
 // behaviour are specified in include/echo.h.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -24,6 +25,7 @@ using echo::grid_of;
 using echo::kMaxRows;
 
 constexpr int64_t kMaxStride = int64_t(1) << 40;        // of pages and heads, in elements
+constexpr int64_t kMaxLen = (int64_t(1) << 31) - (1 << 12);     // positions and the tiles behind them stay in 31 bits
 constexpr int64_t kCus = 256;
 
 int check_cache(const echo_cache& c)
@@ -83,7 +85,7 @@ echo::SeqView seq_view(const echo_seqs& s, const echo_cache& c)
     std::memset(&v, 0, sizeof(v));
     v.starts = s.starts; v.lens = s.lens; v.table = s.page_table;
     v.ld_table = s.ld_table; v.table_pages = s.table_pages;
-    v.capacity = s.table_pages * c.page_tokens;             // below 2^62
+    v.capacity = std::min(s.table_pages * c.page_tokens, kMaxLen);          // the product is below 2^62
     v.seqs = (int)s.seqs; v.tokens = s.tokens;
     return v;
 }
@@ -145,36 +147,42 @@ int cache_io(const echo_cache* c, const echo_seqs* s, void* k, int64_t ld_k, voi
 
 // How a call is split.
 struct AttnPlan {
-    int64_t tiles;          // row tiles of a sequence with a block of their own
+    bool few, tile;         // which kernels run; with both, a sequence of few rows is the former's
+    int64_t few_tiles, tile_tiles;      // row tiles of a sequence with a block of their own
     int splits;             // parts of a row's tokens
     size_t part_ml, total;  // of the workspace: the parts' sums of v, then their m and l
 };
 
-constexpr int64_t kFewBlocks = 4 * kCus, kFewPart = 256, kMostSplits = 256;
+constexpr int64_t kTileRows = 32 * echo::kTileWaves;
+constexpr int64_t kFewBlocks = 4 * kCus, kFewPart = 256, kTileBlocks = 2 * kCus, kTilePart = 512, kMostSplits = 256;
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 AttnPlan attn_plan(const echo_attention_args& p)
 {
     AttnPlan n = {};
-    const int64_t G = p.q_heads / p.cache.heads;
-    const int64_t most_new = p.seqs.max_new < 1 ? 1 : (p.seqs.max_new < p.seqs.tokens ? p.seqs.max_new : p.seqs.tokens);
-    const int64_t capacity = p.seqs.table_pages * p.cache.page_tokens;
-    int64_t len = p.seqs.max_len < capacity ? p.seqs.max_len : capacity;
-    n.tiles = (most_new * G + echo::kFewRows - 1) / echo::kFewRows;
-    if (p.window > 0 && p.window < len - 16) len = p.window + 16;          // of a row tile's rows together
-    const int64_t blocks = n.tiles * p.seqs.seqs * p.cache.heads;
-    int64_t splits = (kFewBlocks + blocks - 1) / blocks;
-    if (splits > (len + kFewPart - 1) / kFewPart) splits = (len + kFewPart - 1) / kFewPart;
-    if (splits > kMostSplits) splits = kMostSplits;
-    if (splits < 1) splits = 1;
-    // a launch's blocks are 32 bits: the kernel strides over the row tiles
-    const int64_t most = (int64_t(1) << 24) / (p.seqs.seqs * p.cache.heads);
-    if (splits > 1 && n.tiles * splits > most) splits = 1;
-    if (n.tiles > most) n.tiles = most < 1 ? 1 : most;
-    n.splits = (int)splits;
-    if (splits > 1) {
-        const int64_t rows = p.seqs.tokens * p.q_heads;
-        n.part_ml = (size_t)(rows * splits * p.cache.width * 4);
-        n.total = n.part_ml + (size_t)(rows * splits * 8);
+    const int64_t G = p.q_heads / p.cache.heads, T = p.seqs.tokens, pairs = p.seqs.seqs * p.cache.heads;
+    const int64_t most_new = std::max<int64_t>(1, std::min(p.seqs.max_new, T));
+    n.tile = most_new * G > echo::kFewRows;
+    n.few = !n.tile || p.seqs.seqs > 1;
+    n.few_tiles = n.tile ? 1 : ceil_div(most_new * G, echo::kFewRows);
+    n.tile_tiles = ceil_div(most_new * G, kTileRows);
+    // tokens that a row tile sees at most
+    int64_t len = std::min(p.seqs.max_len, p.seqs.table_pages * p.cache.page_tokens);
+    if (p.window > 0) len = std::min(len, std::min(p.window, len) + ceil_div(n.tile ? kTileRows : echo::kFewRows, G));
+    // blocks that have work, as far as the host can tell
+    const int64_t blocks = n.tile ? std::max<int64_t>(1, T * G / kTileRows) * p.cache.heads : n.few_tiles * pairs;
+    int64_t splits = ceil_div(n.tile ? kTileBlocks : kFewBlocks, blocks);
+    splits = std::min(splits, std::min(ceil_div(len, n.tile ? kTilePart : kFewPart), kMostSplits));
+    // a launch's blocks are 32 bits: the kernels stride over the row tiles
+    const int64_t most = std::max<int64_t>(1, (int64_t(1) << 24) / pairs);
+    n.splits = (int)std::max<int64_t>(1, std::min(splits, most));
+    n.few_tiles = std::max<int64_t>(1, std::min(n.few_tiles, most / n.splits));
+    n.tile_tiles = std::max<int64_t>(1, std::min(n.tile_tiles, most / n.splits));
+    if (n.splits > 1) {
+        const int64_t rows = T * p.q_heads;
+        n.part_ml = (size_t)(rows * n.splits * p.cache.width * 4);
+        n.total = n.part_ml + (size_t)(rows * n.splits * 8);
     }
     return n;
 }
@@ -194,19 +202,31 @@ int check_attention(const echo_attention_args* p)
 }
 
 template <int KIND, int DP>
-void attention_few_go(const echo::AttnArgs& a, int64_t blocks, hipStream_t st)
+void attention_go(echo::AttnArgs& a, const AttnPlan& n, hipStream_t st)
 {
-    const dim3 grid((unsigned)blocks), block(64 * echo::kFewAttnWaves);
-    if (a.c.page_tokens % 16) hipLaunchKernelGGL((echo::attention_few_kernel<KIND, DP, false>), grid, block, 0, st, a);
-    else hipLaunchKernelGGL((echo::attention_few_kernel<KIND, DP, true>), grid, block, 0, st, a);
+    const bool page16 = a.c.page_tokens % 16 == 0;
+    const int64_t pairs = (int64_t)a.s.seqs * a.c.heads * n.splits;
+    a.few_rows = n.few && n.tile ? echo::kFewRows : 0;
+    if (n.tile) {
+        a.tiles = (uint32_t)n.tile_tiles;
+        const dim3 grid((unsigned)(n.tile_tiles * pairs)), block(64 * echo::kTileWaves);
+        if (page16) hipLaunchKernelGGL((echo::attention_tile_kernel<KIND, DP, 1, true>), grid, block, 0, st, a);
+        else hipLaunchKernelGGL((echo::attention_tile_kernel<KIND, DP, 1, false>), grid, block, 0, st, a);
+    }
+    if (n.few) {
+        a.tiles = (uint32_t)n.few_tiles;
+        const dim3 grid((unsigned)(n.few_tiles * pairs)), block(64 * echo::kFewAttnWaves);
+        if (page16) hipLaunchKernelGGL((echo::attention_few_kernel<KIND, DP, true>), grid, block, 0, st, a);
+        else hipLaunchKernelGGL((echo::attention_few_kernel<KIND, DP, false>), grid, block, 0, st, a);
+    }
 }
 
 template <int KIND>
-void attention_few(const echo::AttnArgs& a, int64_t blocks, hipStream_t st)
+void attention_sized(echo::AttnArgs& a, const AttnPlan& n, hipStream_t st)
 {
-    if (a.c.width <= 64) attention_few_go<KIND, 64>(a, blocks, st);
-    else if (a.c.width <= 128) attention_few_go<KIND, 128>(a, blocks, st);
-    else attention_few_go<KIND, 256>(a, blocks, st);
+    if (a.c.width <= 64) attention_go<KIND, 64>(a, n, st);
+    else if (a.c.width <= 128) attention_go<KIND, 128>(a, n, st);
+    else attention_go<KIND, 256>(a, n, st);
 }
 
 }  // namespace
@@ -246,18 +266,16 @@ int echo_cache_attention(const echo_attention_args* p, void* workspace, size_t w
     a.c = cache_view(p->cache);
     a.s = seq_view(p->seqs, p->cache);
     a.q = p->q; a.out = p->out; a.lse = p->lse; a.ld_q = p->ld_q; a.ld_out = p->ld_out;
-    a.window = p->window; a.group = (int)(p->q_heads / p->cache.heads); a.causal = p->causal;
+    a.window = (int)std::min(p->window, kMaxRows); a.group = (int)(p->q_heads / p->cache.heads); a.causal = p->causal;
     a.scale2 = (float)((double)p->scale * 1.4426950408889634);
     a.splits = plan.splits;
-    a.tiles = (uint32_t)plan.tiles;
     a.part_o = (float*)workspace;
     a.part_ml = (float*)((uint8_t*)workspace + plan.part_ml);
     const hipStream_t st = (hipStream_t)stream;
-    const int64_t blocks = plan.tiles * plan.splits * p->seqs.seqs * p->cache.heads;
     switch (p->cache.kind) {
-    case ECHO_BF16: attention_few<echo::kCacheBf16>(a, blocks, st); break;
-    case ECHO_I8: attention_few<echo::kCacheI8>(a, blocks, st); break;
-    default: attention_few<echo::kCacheI4>(a, blocks, st); break;
+    case ECHO_BF16: attention_sized<echo::kCacheBf16>(a, plan, st); break;
+    case ECHO_I8: attention_sized<echo::kCacheI8>(a, plan, st); break;
+    default: attention_sized<echo::kCacheI4>(a, plan, st); break;
     }
     if ((rc = check_launch()) || plan.splits == 1) return rc;
     const int64_t rows = p->seqs.tokens * p->q_heads;

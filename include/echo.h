@@ -589,8 +589,8 @@ typedef struct echo_cache {
  *
  * These arrays are read on the device and cannot be checked by the host.  The
  * kernels read and write nothing outside the buffers whatever they hold: a
- * token has no place where its position is negative or its entry of the table
- * is past table_pages or names no page.  A sequence whose rows are not all
+ * token has no place where its position is negative or 2^31 - 2^12 and more, or
+ * its entry of the table is past table_pages or names no page.  A sequence whose rows are not all
  * among 0 .. tokens - 1 is not taken; rows of no sequence are left as they were.
  * max_new and max_len (the most rows and the greatest length of a sequence)
  * decide how work is split.  Results are right, but slower, where they are
