@@ -58,10 +58,11 @@ __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_ex
 __device__ __forceinline__ float nan_f32() { return __builtin_bit_cast(float, 0x7FC00000u); }
 __device__ __forceinline__ float neg_inf() { return -__builtin_inff(); }
 
-// largest / sum over the four 16-lane rows of a wave (lanes that share lane % 16)
-__device__ __forceinline__ float rows4_max(float v)
+// largest / sum over the lanes that share a query row: lane % 16 with ROWS = 4, lane % 32 with 2
+template <int ROWS>
+__device__ __forceinline__ float rows_max(float v)
 {
-    v = fmaxf(v, __shfl_xor(v, 16));
+    if constexpr (ROWS == 4) v = fmaxf(v, __shfl_xor(v, 16));
     return fmaxf(v, __shfl_xor(v, 32));
 }
 __device__ __forceinline__ float rows4_sum(float v)
@@ -80,10 +81,11 @@ struct RowSpan {
 };
 __device__ __forceinline__ RowSpan seq_span(const SeqView& s, int b)
 {
+    // one sequence to a block: said to the compiler, which sees loads
     RowSpan r;
-    const int e = s.starts[b + 1];
-    r.row0 = s.starts[b];
-    r.len = max(s.lens[b], 0);
+    const int e = __builtin_amdgcn_readfirstlane(s.starts[b + 1]);
+    r.row0 = __builtin_amdgcn_readfirstlane(s.starts[b]);
+    r.len = __builtin_amdgcn_readfirstlane(max(s.lens[b], 0));
     r.n = r.row0 < 0 || e > s.tokens || e < r.row0 ? 0 : e - r.row0;
     return r;
 }
@@ -105,6 +107,47 @@ __device__ __forceinline__ void split_span(int splits, int split, int& begin, in
     const int64_t from = min(begin + split * per, (int64_t)end);
     end = (int)min(from + per, (int64_t)end);
     begin = (int)from;
+}
+
+// A row's reference m and its sum l.  Scores come as z = y - m straight from
+// one fma; m follows the largest score when that is 2^8 above it, which leaves
+// most tiles without a rescaling, and weights of up to 2^8 are as exact as any.
+// Rows are raised one by one, so that no row's rounding goes by another's.
+struct RowSum {
+    float minus_m = 0.0f;   // 0 before the first score
+    float over = -__builtin_inff();     // raise m where z passes this: kRaise, before the first score -infinity
+    float l = 0.0f;
+    __device__ __forceinline__ float m() const { return over < 0.0f ? neg_inf() : -minus_m; }
+};
+
+// Makes room for scores z (N of a lane's row, the largest top): afterwards
+// none is over kRaise.  scale(f) multiplies what was summed before.
+template <int ROWS, int N, typename F>
+__device__ __forceinline__ void row_raise(RowSum& r, float (&z)[N], float top, F scale)
+{
+    if (__any(top > r.over)) {
+        top = rows_max<ROWS>(top);
+        const bool up = top > r.over;
+        const float by = up ? top : 0.0f;
+        const float f = up ? (r.over < 0.0f ? 0.0f : exp2_fast(-by)) : 1.0f;
+        r.minus_m -= by;
+        r.over = up ? kRaise : r.over;
+        r.l *= f;
+#pragma unroll
+        for (int v = 0; v < N; ++v) z[v] -= by;
+        scale(f);
+    }
+}
+
+// 8 floats as bfloat16, two to an instruction
+__device__ __forceinline__ bf16x8 to_bf16x8(const float* p)
+{
+    bf16x2 w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = bf16x2{(__bf16)p[2 * i], (__bf16)p[2 * i + 1]};
+    bf16x8 r;
+    __builtin_memcpy(&r, w, 16);
+    return r;
 }
 
 // Out and lse of a row whose sums are whole; sees_past: it sees a token that
@@ -142,7 +185,6 @@ struct FewTile {
     uint32_t k[2][S::kLoads][S::kKWords];
     uint32_t v[8][S::kPieces][S::kVWords];
     uint32_t ks[8], vs[8];      // of the lane's 8 tokens
-    uint32_t bad;               // its tokens without a place, by bits
 };
 
 // 8 elements of k (words) as bfloat16
@@ -190,10 +232,17 @@ __device__ __forceinline__ uint32_t not_finite2(uint32_t w)
     return m | ((w & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u);
 }
 
+// waves on a SIMD that the registers of two tiles leave room for
+constexpr int few_waves(int kind, int dp)
+{
+    return dp == 64 ? (kind == kCacheI4 ? 4 : 3) : (dp == 128 ? (kind == kCacheI4 ? 3 : 2) : (kind == kCacheBf16 ? 1 : 2));
+}
+
 // PAGE16: pages are a multiple of 16 tokens, so the 16 tokens of a tile's half
 // lie in one page; otherwise every lane looks its tokens up.
 template <int KIND, int DP, bool PAGE16>
-__global__ __launch_bounds__(64 * kFewAttnWaves) void attention_few_kernel(const AttnArgs a)
+__global__ __launch_bounds__(64 * kFewAttnWaves) __attribute__((amdgpu_waves_per_eu(few_waves(KIND, DP))))
+void attention_few_kernel(const AttnArgs a)
 {
     using S = FewShape<KIND, DP>;
     constexpr int kFrags = S::kPieces * S::kVE;
@@ -215,6 +264,9 @@ __global__ __launch_bounds__(64 * kFewAttnWaves) void attention_few_kernel(const
     if (a.few_rows && rows > a.few_rows) return;         // the other kernel's
     const uint8_t* kb = c.k + cache_bytes<KIND>(h * c.ld_head);
     const uint8_t* vb = c.v + cache_bytes<KIND>(h * c.ld_head);
+    const int64_t token_bytes = cache_bytes<KIND>(c.ld_token);
+    const uint32_t koff = (uint32_t)(col * token_bytes + cache_bytes<KIND>(S::kE * g));      // for PAGE16, whose host check
+    const uint32_t voff = (uint32_t)(4 * g * token_bytes + cache_bytes<KIND>(S::kVE * col)); // keeps them in 32 bits
 
     for (int64_t rt = id / (uint32_t)a.s.seqs; rt * kFewRows < rows; rt += a.tiles) {
         // this lane's row
@@ -250,80 +302,111 @@ __global__ __launch_bounds__(64 * kFewAttnWaves) void attention_few_kernel(const
         }
         if constexpr (KIND == kCacheI4) qsum = rows4_sum(qsum);
 
-        auto load = [&](FewTile<KIND, DP>& f, int p0) {
-            // where the lane's tokens lie: of k two, of v (and the scores) 8
-            int64_t ko[2], vo[8], sc[8];
-            f.bad = 0;
+        // Page numbers come a tile before the loads that need them.
+        struct Pages {
+            int32_t n[PAGE16 ? 2 : 10];
+        };
+        auto entry_of = [&](int p) { return (uint32_t)min(p, end - 1) / c.page_tokens; };
+        auto lookup = [&](int p0) __attribute__((always_inline)) {
+            Pages pg;
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 if constexpr (PAGE16) {
-                    const uint32_t p = (uint32_t)min(p0 + 16 * u, end - 1);
-                    const uint32_t entry = p / c.page_tokens;
-                    const int32_t page = __builtin_amdgcn_readfirstlane(cache_page(a.s, c, b, entry));
-                    if (page < 0) f.bad |= 15u << (4 * u);
-                    const int64_t pg = page < 0 ? 0 : page;
-                    const uint32_t slot = (p - entry * c.page_tokens) & ~15u;
-                    ko[u] = pg * c.ld_page + (int64_t)(slot + col) * c.ld_token;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        vo[4 * u + e] = pg * c.ld_page + (int64_t)(slot + 4 * g + e) * c.ld_token;
-                        sc[4 * u + e] = pg * c.ld_sp + h * c.ld_sh + slot + 4 * g + e;
-                    }
+                    pg.n[u] = cache_page(a.s, c, b, entry_of(p0 + 16 * u));
                 } else {
-                    auto place = [&](int at, int64_t& o, int64_t& s) {
-                        const uint32_t p = (uint32_t)min(at, end - 1);
-                        const uint32_t entry = p / c.page_tokens;
-                        const int32_t page = cache_page(a.s, c, b, entry);
-                        const int64_t pg = page < 0 ? 0 : page;
-                        const uint32_t slot = p - entry * c.page_tokens;
-                        o = pg * c.ld_page + (int64_t)slot * c.ld_token;
-                        s = pg * c.ld_sp + h * c.ld_sh + slot;
-                        return page < 0;
-                    };
-                    int64_t none;
-                    place(p0 + 16 * u + col, ko[u], none);
+                    pg.n[8 + u] = cache_page(a.s, c, b, entry_of(p0 + 16 * u + col));
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (place(p0 + 16 * u + 4 * g + e, vo[4 * u + e], sc[4 * u + e])) f.bad |= 1u << (4 * u + e);
+                    for (int e = 0; e < 4; ++e) pg.n[4 * u + e] = cache_page(a.s, c, b, entry_of(p0 + 16 * u + 4 * g + e));
                 }
             }
+            return pg;
+        };
+        // one token's k (load j) and v; at: 8 elements, or what is left of the width
+        auto take_k = [&](uint32_t (&w)[S::kKWords], const uint8_t* at, int j) __attribute__((always_inline)) {
+            const int d = S::kE * (4 * j + g);
+            if (d + S::kE <= c.width) {
+                __builtin_memcpy(w, __builtin_assume_aligned(at, 4), 4 * S::kKWords);
+            } else {                                         // q is 0 past the width, and so has k to be
+                constexpr int kWords8 = S::kKWords * 8 / S::kE;             // of 8 elements
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
+                for (int i = 0; i < S::kKWords; ++i) w[i] = d + i / kWords8 * 8 < c.width ? ((const uint32_t*)at)[i] : 0u;
+            }
+        };
+        auto take_v = [&](uint32_t (&w)[S::kVWords], const uint8_t* at, int p) __attribute__((always_inline)) {
 #pragma unroll
-                for (int j = 0; j < S::kLoads; ++j) {
-                    const int d = S::kE * (4 * j + g);
-                    const uint8_t* from = kb + cache_bytes<KIND>(ko[u] + d);
-                    if (d + S::kE <= c.width) {
-                        __builtin_memcpy(f.k[u][j], __builtin_assume_aligned(from, 4), 4 * S::kKWords);
-                    } else {                                 // q is 0 past the width, and so has k to be
-                        constexpr int kWords8 = S::kKWords * 8 / S::kE;     // of 8 elements
+            for (int i = 0; i < S::kVWords; ++i) w[i] = 0;
+            if (128 * p + S::kVE * col < c.width) __builtin_memcpy(w, at, S::kVBytes);
+        };
+        constexpr int kLoadBytes = 4 * 4 * S::kKWords;       // of k, from one load of a lane to its next
+        constexpr int kPieceBytes = 16 * S::kVBytes;
+        auto load = [&](FewTile<KIND, DP>& f, int p0, const Pages& pg) __attribute__((always_inline)) {
+            uint32_t kbad = 0, bad = 0;                      // tokens without a place, by bits: their scores are NaN
+            if constexpr (PAGE16) {
+                // a base for 16 tokens in scalar registers, and the lane's offsets
 #pragma unroll
-                        for (int w = 0; w < S::kKWords; ++w)
-                            f.k[u][j][w] = d + w / kWords8 * 8 < c.width ? ((const uint32_t*)from)[w] : 0u;
+                for (int u = 0; u < 2; ++u) {
+                    const int32_t page = __builtin_amdgcn_readfirstlane(pg.n[u]);
+                    if (page < 0) bad |= 15u << (4 * u), kbad |= 1u << u;
+                    const int64_t at = page < 0 ? 0 : page;
+                    const uint32_t slot = (uint32_t)min(p0 + 16 * u, end - 1) % c.page_tokens & ~15u;
+                    const int64_t row = cache_bytes<KIND>(at * c.ld_page + slot * c.ld_token);
+                    const uint8_t *kr = kb + row, *vr = vb + row;
+#pragma unroll
+                    for (int j = 0; j < S::kLoads; ++j) take_k(f.k[u][j], kr + j * kLoadBytes + koff, j);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+#pragma unroll
+                        for (int p = 0; p < S::kPieces; ++p) take_v(f.v[4 * u + e][p], vr + e * token_bytes + p * kPieceBytes + voff, p);
+                    if constexpr (KIND != kCacheBf16) {
+                        const int64_t sr = at * c.ld_sp + h * c.ld_sh + slot;
+                        __builtin_memcpy(&f.ks[4 * u], (const uint8_t*)(c.ks + sr) + 16u * g, 16);
+                        __builtin_memcpy(&f.vs[4 * u], (const uint8_t*)(c.vs + sr) + 16u * g, 16);
                     }
                 }
+            } else {
+                auto place = [&](int t, int32_t page, int64_t& o, int64_t& s) __attribute__((always_inline)) {
+                    const uint32_t slot = (uint32_t)min(t, end - 1) % c.page_tokens;
+                    const int64_t at = page < 0 ? 0 : page;
+                    o = at * c.ld_page + (int64_t)slot * c.ld_token;
+                    s = at * c.ld_sp + h * c.ld_sh + slot;
+                    return page < 0;
+                };
+                int64_t o, s;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
+                for (int u = 0; u < 2; ++u) {
+                    if (place(p0 + 16 * u + col, pg.n[8 + u], o, s)) kbad |= 1u << u;
 #pragma unroll
-                for (int p = 0; p < S::kPieces; ++p) {
-                    const int d = 128 * p + S::kVE * col;
-#pragma unroll
-                    for (int w = 0; w < S::kVWords; ++w) f.v[e][p][w] = 0;
-                    if (d < c.width) __builtin_memcpy(f.v[e][p], vb + cache_bytes<KIND>(vo[e] + d), S::kVBytes);
+                    for (int j = 0; j < S::kLoads; ++j) take_k(f.k[u][j], kb + cache_bytes<KIND>(o + S::kE * (4 * j + g)), j);
                 }
-                if constexpr (KIND != kCacheBf16) {
-                    f.ks[e] = c.ks[sc[e]];
-                    f.vs[e] = c.vs[sc[e]];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    if (place(p0 + 16 * (e / 4) + 4 * g + (e & 3), pg.n[e], o, s)) bad |= 1u << e;
+#pragma unroll
+                    for (int p = 0; p < S::kPieces; ++p) take_v(f.v[e][p], vb + cache_bytes<KIND>(o + 128 * p + S::kVE * col), p);
+                    if constexpr (KIND != kCacheBf16) {
+                        f.ks[e] = c.ks[s];
+                        f.vs[e] = c.vs[s];
+                    }
                 }
+            }
+            if (__any((bad | kbad) != 0)) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (KIND != kCacheBf16 && (bad >> e) & 1u) f.ks[e] = KIND == kCacheI8 ? 0x7FC00000u : 0x7E00u;
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+                    if (KIND == kCacheBf16 && (kbad >> u) & 1u) f.k[u][0][0] = 0x7FC07FC0u;
             }
         };
 
         f32x4 o[kFrags];
 #pragma unroll
         for (int f = 0; f < kFrags; ++f) o[f] = f32x4{0, 0, 0, 0};
-        float m = neg_inf(), l = 0.0f, off = 0.0f;           // off: what the codes' offsets add to every element
+        int p0 = begin + kFewTile * (int)wave;
+        RowSum sum;
+        float off = 0.0f;                                    // what the codes' offsets add to every element
 
-        auto take = [&](FewTile<KIND, DP>& f, int p0) {
+        auto take = [&](FewTile<KIND, DP>& f) __attribute__((always_inline)) {
             f32x4 acc[2];
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
@@ -335,30 +418,26 @@ __global__ __launch_bounds__(64 * kFewAttnWaves) void attention_few_kernel(const
                                                                      fq[st], acc[u], 0, 0, 0);
                 }
             }
-            float x[8];
+            float z[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const float s = acc[e / 4][e % 4];
-                if constexpr (KIND == kCacheBf16) x[e] = s * a.scale2;
-                else if constexpr (KIND == kCacheI8) x[e] = s * (__builtin_bit_cast(float, f.ks[e]) * a.scale2);
-                else x[e] = __builtin_fmaf(-(16.0f + half_hi(f.ks[e])), qsum, s) * (half_lo(f.ks[e]) * a.scale2);
+                if constexpr (KIND == kCacheBf16) z[e] = __builtin_fmaf(s, a.scale2, sum.minus_m);
+                else if constexpr (KIND == kCacheI8) z[e] = __builtin_fmaf(s, __builtin_bit_cast(float, f.ks[e]) * a.scale2, sum.minus_m);
+                else z[e] = __builtin_fmaf(__builtin_fmaf(-(16.0f + half_hi(f.ks[e])), qsum, s), half_lo(f.ks[e]) * a.scale2, sum.minus_m);
             }
-            // which of the tile's tokens the row sees
-            const bool whole = __all(!there || (lo <= p0 && p0 + kFewTile - 1 <= hi)) && p0 + kFewTile <= end;
-            uint32_t odd = 0, seen = 255;                    // tokens whose v holds no number; that the row sees
-            const bool bad = __any(f.bad != 0);
-            if (!whole || bad) {
+            // The mask costs every tile three instructions a score; tiles of two
+            // kinds would cost the registers of another tile on its way.
+            const uint32_t from = lo - p0 - 4 * g, span = min(hi, end - 1) - lo;     // a row that sees nothing has a span below -1
+            bool sees[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int p = p0 + 16 * (e / 4) + 4 * g + (e & 3);
-                    const bool sees = p >= lo && p <= hi && p < end;
-                    if ((f.bad >> e) & 1u) x[e] = nan_f32();
-                    if (!sees) {
-                        x[e] = neg_inf();
-                        seen &= ~(1u << e);
-                    }
-                }
-                if constexpr (KIND == kCacheBf16) {
+            for (int e = 0; e < 8; ++e) {
+                sees[e] = 16u * (e / 4) + (e & 3) - from <= span && (int)span >= 0;
+                z[e] = sees[e] ? z[e] : neg_inf();
+            }
+            uint32_t odd = 0;                                // tokens whose v holds no number
+            if constexpr (KIND == kCacheBf16) {
+                if (!(__all(!there || (lo <= p0 && p0 + kFewTile - 1 <= hi)) && p0 + kFewTile <= end)) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
 #pragma unroll
@@ -372,38 +451,29 @@ __global__ __launch_bounds__(64 * kFewAttnWaves) void attention_few_kernel(const
                     odd = group_fold<16>(odd, [](uint32_t p, uint32_t q) { return p | q; });
                 }
             }
-            float top = x[0];
+            float top = z[0];
 #pragma unroll
-            for (int e = 1; e < 8; ++e) top = fmaxf(top, x[e]);
-            if (__any(top > m + kRaise)) {
-                // row by row, so that no row's rounding goes by another's scores
-                top = rows4_max(top);
-                const float up = top > m + kRaise ? top : m;
-                const float fac = up == m ? 1.0f : exp2_fast(m - up);
-                m = up;
-                l *= fac;
-                off *= fac;
+            for (int e = 1; e < 8; ++e) top = fmaxf(top, z[e]);
+            row_raise<4>(sum, z, top, [&](float by) {
+                off *= by;
 #pragma unroll
-                for (int j = 0; j < kFrags; ++j) o[j] *= fac;
-            }
-            const float base = m == neg_inf() ? 0.0f : m;
+                for (int j = 0; j < kFrags; ++j) o[j] *= by;
+            });
             float p[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                p[e] = exp2_fast(x[e] - base);
-                l += p[e];
-                const bool sees = (seen >> e) & 1u;
-                if constexpr (KIND == kCacheI8) p[e] = sees ? p[e] * __builtin_bit_cast(float, f.vs[e]) : 0.0f;
-                if constexpr (KIND == kCacheI4) p[e] = sees ? p[e] * half_lo(f.vs[e]) : 0.0f;
-                if (KIND == kCacheBf16 && sees && ((odd >> e) & 1u)) p[e] = nan_f32();
+                p[e] = exp2_fast(z[e]);
+                sum.l += p[e];
+                if constexpr (KIND == kCacheI8) p[e] *= __builtin_bit_cast(float, f.vs[e]);
+                if constexpr (KIND == kCacheI4) p[e] *= half_lo(f.vs[e]);
+                if (KIND == kCacheBf16 && ((odd >> e) & 1u)) p[e] = nan_f32();
+                p[e] = sees[e] ? p[e] : 0.0f;
             }
-            bf16x8 fp;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) fp[e] = (__bf16)p[e];
+            const bf16x8 fp = to_bf16x8(p);
             if constexpr (KIND == kCacheI4) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    if ((seen >> e) & 1u) off = __builtin_fmaf((float)fp[e], 16.0f + half_hi(f.vs[e]), off);
+                    off = __builtin_fmaf((float)fp[e], sees[e] ? 16.0f + half_hi(f.vs[e]) : 0.0f, off);
             }
 #pragma unroll
             for (int pc = 0; pc < S::kPieces; ++pc) {
@@ -418,14 +488,34 @@ __global__ __launch_bounds__(64 * kFewAttnWaves) void attention_few_kernel(const
                                                                                o[S::kVE * pc + j], 0, 0, 0);
             }
         };
-        for (int p0 = begin + kFewTile * (int)wave; p0 < end; p0 += kFewTile * kFewAttnWaves) {
+        constexpr int kStep = kFewTile * kFewAttnWaves;
+        constexpr bool kAhead = DP < 256;                    // the next tile is on its way while one is multiplied
+        if (p0 < end) {
             FewTile<KIND, DP> f;
-            load(f, p0);
-            take(f, p0);
+            Pages pg = lookup(p0);
+            if constexpr (kAhead) {
+                load(f, p0, pg);
+                pg = lookup(p0 + kStep);
+                while (p0 + kStep < end) {
+                    FewTile<KIND, DP> next;
+                    load(next, p0 + kStep, pg);
+                    pg = lookup(p0 + 2 * kStep);
+                    take(f);
+                    p0 += kStep;
+                    f = next;
+                }
+                take(f);
+            } else {
+                for (; p0 < end; p0 += kStep) {
+                    load(f, p0, pg);
+                    pg = lookup(p0 + kStep);
+                    take(f);
+                }
+            }
         }
 
         // the waves' sums to the largest m
-        l = rows4_sum(l);
+        const float m = sum.m(), l = rows4_sum(sum.l);
         if constexpr (KIND == kCacheI4) off = rows4_sum(off);
         if (g == 0) {
             sm[wave][col] = m;
@@ -500,9 +590,9 @@ __global__ __launch_bounds__(64 * kFewAttnWaves) void attention_few_kernel(const
 // as the second one's operand, and so that the writes of 16 lanes fall on
 // consecutive words; k's words are spread by an exclusive or.
 
-template <int DP>
+template <int DP, int W>
 struct TileShape {
-    static constexpr int kTokens = 8192 / DP;            // of a tile
+    static constexpr int kTokens = 2048 * W / DP;        // of a tile
     static constexpr int kUnits = DP / 8;                // of 8 elements
     static constexpr int kSubs = kTokens / 32;           // 32 tokens: the rows of a first product
     static constexpr int kSteps = kTokens / 16;          // 16 tokens: the depth of a second one
@@ -510,7 +600,26 @@ struct TileShape {
     static constexpr int kEach = 32 / kUnits;            // elements of a unit in a part
 };
 
-constexpr int kTileWaves = 4;
+// f(0) .. f(7) with the number as a constant
+template <typename F>
+__device__ __forceinline__ void unroll8(F f)
+{
+    using std::integral_constant;
+    f(integral_constant<int, 0>{}); f(integral_constant<int, 1>{}); f(integral_constant<int, 2>{}); f(integral_constant<int, 3>{});
+    f(integral_constant<int, 4>{}); f(integral_constant<int, 5>{}); f(integral_constant<int, 6>{}); f(integral_constant<int, 7>{});
+}
+
+// v of lane E of the octet's lanes (8, or the 16 of a row, of which every
+// eighth holds the same): a broadcast within the row
+template <int UNITS, int E>
+__device__ __forceinline__ float octet_lane(float v)
+{
+    const int i = __builtin_bit_cast(int, v);
+    const int a = dpp_i<0x150 + E>(i);                       // row_newbcast
+    if constexpr (UNITS >= 16) return __builtin_bit_cast(float, a);
+    const int b = dpp_i<0x158 + E>(i);
+    return __builtin_bit_cast(float, threadIdx.x & 8u ? b : a);
+}
 
 template <int KIND>
 struct RawUnit {                                         // 8 elements as they lie in the cache
@@ -526,46 +635,60 @@ __device__ __forceinline__ float unit_get(const RawUnit<KIND>& r, int e, float z
     else return (float)((r.w[0] >> (4 * e)) & 15u) - z;
 }
 
-template <int KIND, int DP, int QR, bool PAGE16>
-__global__ __launch_bounds__(64 * kTileWaves) __attribute__((amdgpu_waves_per_eu(DP == 256 ? 1 : 2, DP == 256 ? 1 : 2)))
+template <int KIND, int DP, int W, int QR, bool PAGE16>
+__global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(DP == 256 ? 1 : 2, DP == 256 ? 1 : 2)))
 void attention_tile_kernel(const AttnArgs a)
 {
-    using S = TileShape<DP>;
-    constexpr int kRows = 32 * QR * kTileWaves;
+    using S = TileShape<DP, W>;
+    constexpr int kRows = 32 * QR * W;
     constexpr int kWords = S::kTokens * DP / 8;          // of 16 bytes, in a stage of k or v
     __shared__ __align__(16) u32x4 sk[2][kWords], sv[2][kWords];
     __shared__ __align__(16) float sks[2][S::kTokens], svs[2][S::kTokens];      // k's scale times scale2, v's scale
-    __shared__ __align__(16) uint8_t sbad[2][2 * S::kSteps], sodd[2][2 * S::kSteps];          // by halves of 16 tokens, as v's units
+    __shared__ uint8_t sodd[2][2 * S::kSteps];           // tokens whose v holds no number, by v's octets
     const CacheView& c = a.c;
     const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int col = lane & 31, half = lane >> 5;
-    // blocks of one sequence and head follow each other at a distance of all of
-    // them, so that they share an XCD's cache where their number is a multiple
-    // of 8; a sequence's last rows, which see the most, come first
+    // Heads are the fastest number: where they are a multiple of 8, all blocks
+    // of a head share an XCD's cache.  Row tiles have numbers by their first
+    // row in the whole call plus one for each sequence, so that the launch
+    // needs no count of them and those that are there follow each other (with
+    // blocks that have nothing to do between them, a chunk of 512 tokens beside
+    // 7 single ones took 390 us, in this order 170); a sequence's last rows,
+    // which see the most, come first.
     uint32_t id = blockIdx.x;
-    const uint32_t pairs = (uint32_t)c.heads * (uint32_t)a.s.seqs;
-    const int h = (id % pairs) % (uint32_t)c.heads, b = (id % pairs) / (uint32_t)c.heads;
-    id /= pairs;
-    const int split = id % (uint32_t)a.splits;
-    id /= (uint32_t)a.splits;
+    const int h = id % (uint32_t)c.heads;
+    id /= (uint32_t)c.heads;
+    const int64_t v = id % a.tiles;
+    const int split = id / a.tiles;
+    auto tile_base = [&](int b) { return (int64_t)a.s.starts[b] * a.group / kRows + b; };
+    int b = 0;
+    for (int top = a.s.seqs - 1; b < top;) {             // the last sequence whose tiles start at or below v
+        const int mid = (b + top + 1) >> 1;
+        if (__builtin_amdgcn_readfirstlane(tile_base(mid) <= v)) b = mid;
+        else top = mid - 1;
+    }
+    b = __builtin_amdgcn_readfirstlane(b);
     const RowSpan r = seq_span(a.s, b);
     const int rows = r.n * a.group;                      // below 2^31 with all heads
     if (a.few_rows && rows <= a.few_rows) return;        // the other kernel's
     const uint8_t* kb = c.k + cache_bytes<KIND>(h * c.ld_head);
     const uint8_t* vb = c.v + cache_bytes<KIND>(h * c.ld_head);
 
-    // what this thread stages: a unit of 8 tokens of k (first half of the threads) or of v
-    const bool is_v = tid >= 128;
-    const int su = tid % S::kUnits, so = (tid & 127u) / S::kUnits;               // unit, octet of tokens
-    auto staged_token = [&](int e) { return is_v ? 16 * (so >> 1) + 4 * (so & 1) + (e & 3) + 8 * (e >> 2) : 8 * so + e; };
-    const uint8_t* from = is_v ? vb : kb;
-    const uint32_t* scales = is_v ? c.vs : c.ks;
+    // what this thread stages: a unit of 8 tokens, of k in the first half of
+    // the waves and of v in the others
+    const bool is_v = wave >= W / 2;
+    const int su = tid % S::kUnits, so = (tid & (32 * W - 1)) / S::kUnits;       // unit, octet of tokens
+    const int token0 = is_v ? 16 * (so >> 1) + 4 * (so & 1) : 8 * so;            // of the octet, then
+    auto token_step = [&](int e) { return is_v ? (e & 3) + 8 * (e >> 2) : e; };
+    const uint8_t* from = (is_v ? vb : kb) + cache_bytes<KIND>(8 * su);
+    const uint32_t* scales = (is_v ? c.vs : c.ks) + h * c.ld_sh;
     const bool unit_in = 8 * su < c.width;
+    const int64_t token_bytes = cache_bytes<KIND>(c.ld_token);
 
-    const int64_t row_tiles = (rows + kRows - 1) / kRows;
-    for (int64_t at_tile = id; at_tile < row_tiles; at_tile += a.tiles) {
-        const int64_t rt = row_tiles - 1 - at_tile;
-        // this lane's rows, and of the wave's, whose positions grow
+    const int64_t rt = ((int64_t)rows + kRows - 1) / kRows - 1 - (v - ((int64_t)r.row0 * a.group / kRows + b));
+    if (rt < 0 || rt * kRows >= rows) return;
+    {
+        // this lane's rows
         int hi[QR], lo[QR];
         bf16x8 fq[QR][DP / 16];
 #pragma unroll
@@ -583,14 +706,11 @@ void attention_tile_kernel(const AttnArgs a)
                     bf16x8, ld_raw8<true, false>(a.q, (int64_t)(r.row0 + i) * a.ld_q + (int64_t)qh * c.width, 16 * ks + 8 * half,
                                                  c.width).v[0]);
         }
-        int some_hi = -1, some_lo = INT32_MAX, all_hi = -1, all_lo = 0;   // some row sees some_lo .. some_hi, each all_lo .. all_hi
+        int some_hi = -1, some_lo = INT32_MAX;               // no row sees further than this
         const int64_t first_row = rt * kRows + wave * QR * 32;
         if (first_row < rows) {
-            const int p0 = r.pos((int)first_row / a.group), p1 = r.pos(((int)min(first_row + 32 * QR, (int64_t)rows) - 1) / a.group);
-            all_hi = a.causal ? p0 : r.len - 1;
-            some_hi = a.causal ? p1 : r.len - 1;
-            all_lo = a.window ? p1 - a.window + 1 : 0;
-            some_lo = a.window ? p0 - a.window + 1 : 0;
+            some_hi = a.causal ? r.pos(((int)min(first_row + 32 * QR, (int64_t)rows) - 1) / a.group) : r.len - 1;
+            some_lo = a.window ? r.pos((int)first_row / a.group) - a.window + 1 : 0;
         }
         int begin, end;
         const int i0 = (int)(rt * kRows) / a.group, i1 = ((int)min((int64_t)rows, (rt + 1) * kRows) - 1) / a.group;
@@ -599,60 +719,73 @@ void attention_tile_kernel(const AttnArgs a)
         // tiles inside these bounds are seen whole by every row of the block
         const int block_hi = min(a.causal ? r.pos(i0) : r.len - 1, end - 1);
         const int block_lo = a.window ? r.pos(i1) - a.window + 1 : 0;
+        auto whole = [&](int p0) { return block_lo <= p0 && p0 + S::kTokens - 1 <= block_hi; };
 
         RawUnit<KIND> raw[8];
-        uint32_t word[8];
-        uint32_t bad;
-        auto load = [&](int p0) {
-            bad = 0;
-            int64_t page0 = 0;
-            uint32_t slot0 = 0;
-            if constexpr (PAGE16) {
-                const uint32_t p = (uint32_t)min(p0 + (staged_token(0) & ~15), end - 1);
+        uint32_t word = 0;                                   // scale or parameters of the octet's token su % 8
+        uint32_t bad;                                        // tokens without a place, by bits: their scores are NaN
+        auto load = [&](int p0) __attribute__((always_inline)) {
+            auto lookup = [&](int t, int64_t& page, uint32_t& slot) __attribute__((always_inline)) {
+                const uint32_t p = (uint32_t)min(p0 + t, end - 1);
                 const uint32_t entry = p / c.page_tokens;
-                const int32_t page = cache_page(a.s, c, b, entry);
-                if (page < 0) bad = 255u;
-                page0 = page < 0 ? 0 : page;
-                slot0 = (p - entry * c.page_tokens) & ~15u;
-            }
+                page = cache_page(a.s, c, b, entry);
+                slot = p - entry * c.page_tokens;
+                const bool none = page < 0;
+                page = none ? 0 : page;
+                return none;
+            };
+            int64_t page;
+            uint32_t slot;
+            if constexpr (PAGE16) {
+                bad = lookup(token0 & ~15, page, slot) ? 255u : 0u;
+                slot = (slot & ~15u) + (token0 & 15);
+                if constexpr (KIND != kCacheBf16) word = scales[page * c.ld_sp + slot + token_step(su & 7)];
+                const uint8_t* at = from + cache_bytes<KIND>(page * c.ld_page + slot * c.ld_token);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                if constexpr (!PAGE16) {
-                    const uint32_t p = (uint32_t)min(p0 + staged_token(e), end - 1);
-                    const uint32_t entry = p / c.page_tokens;
-                    const int32_t page = cache_page(a.s, c, b, entry);
-                    if (page < 0) bad |= 1u << e;
-                    page0 = page < 0 ? 0 : page;
-                    slot0 = p - entry * c.page_tokens;
+                for (int e = 0; e < 8; ++e) {
+                    raw[e] = RawUnit<KIND>{};
+                    if (unit_in) __builtin_memcpy(raw[e].w, __builtin_assume_aligned(at, sizeof(raw[e].w)), sizeof(raw[e].w));
+                    at += token_bytes * (e == 3 && is_v ? 5 : 1);
                 }
-                const uint32_t slot = PAGE16 ? slot0 + (staged_token(e) & 15) : slot0;
-                const int64_t at = page0 * c.ld_page + (int64_t)slot * c.ld_token + 8 * su;
-                raw[e] = RawUnit<KIND>{};
-                if (unit_in) __builtin_memcpy(raw[e].w, __builtin_assume_aligned(from + cache_bytes<KIND>(at), sizeof(raw[e].w)), sizeof(raw[e].w));
-                if constexpr (KIND != kCacheBf16) word[e] = scales[page0 * c.ld_sp + h * c.ld_sh + slot];
+            } else {
+                bad = 0;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    if (lookup(token0 + token_step(e), page, slot)) bad |= 1u << e;
+                    raw[e] = RawUnit<KIND>{};
+                    const uint8_t* at = from + cache_bytes<KIND>(page * c.ld_page + slot * c.ld_token);
+                    if (unit_in) __builtin_memcpy(raw[e].w, __builtin_assume_aligned(at, sizeof(raw[e].w)), sizeof(raw[e].w));
+                }
+                if constexpr (KIND != kCacheBf16) {
+                    lookup(token0 + token_step(su & 7), page, slot);
+                    word = scales[page * c.ld_sp + slot];
+                }
             }
         };
-        auto stage = [&](int buf, int p0) {
-            float z[8];
+        auto stage = [&](int buf, int p0) __attribute__((always_inline)) {
+            float z[8];                                      // zero points
+            if constexpr (KIND == kCacheI4) {
+                const float mine = half_hi(word);
+                unroll8([&](auto e) { z[e] = octet_lane<S::kUnits, e>(mine); });
+            } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) z[e] = KIND == kCacheI4 ? half_hi(word[e]) : 0.0f;
-            if (su == 0) {
-                if constexpr (KIND != kCacheBf16) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float s = KIND == kCacheI8 ? __builtin_bit_cast(float, word[e]) : half_lo(word[e]);
-                        (is_v ? svs : sks)[buf][staged_token(e)] = is_v ? s : s * a.scale2;
-                    }
+                for (int e = 0; e < 8; ++e) z[e] = 0.0f;
+            }
+            if constexpr (KIND != kCacheBf16) {
+                if (su < 8) {
+                    float s = KIND == kCacheI8 ? __builtin_bit_cast(float, word) : half_lo(word);
+                    if ((bad >> su) & 1u) s = nan_f32();
+                    (is_v ? svs : sks)[buf][token0 + token_step(su)] = is_v ? s : s * a.scale2;
                 }
-                if (is_v) sbad[buf][so] = (uint8_t)bad;
             }
             if (!is_v) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const int t = 8 * so + e;
+                    const int t = token0 + e;
                     u32x4 o;
                     if constexpr (KIND == kCacheBf16) {
                         o = u32x4{raw[e].w[0], raw[e].w[1], raw[e].w[2], raw[e].w[3]};
+                        if ((bad >> e) & 1u) o = u32x4{0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u};
                     } else {
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
@@ -664,7 +797,7 @@ void attention_tile_kernel(const AttnArgs a)
             }
             if constexpr (KIND == kCacheBf16) {
                 uint32_t odd = 0;
-                if (p0 < block_lo || p0 + S::kTokens - 1 > block_hi) {
+                if (!whole(p0)) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
 #pragma unroll
@@ -693,17 +826,14 @@ void attention_tile_kernel(const AttnArgs a)
         };
 
         f32x16 o[QR][S::kParts];
-        float m[QR], l[QR];
+        RowSum sum[QR];
 #pragma unroll
-        for (int x = 0; x < QR; ++x) {
-            m[x] = neg_inf();
-            l[x] = 0.0f;
+        for (int x = 0; x < QR; ++x)
 #pragma unroll
             for (int p = 0; p < S::kParts; ++p)
 #pragma unroll
                 for (int v = 0; v < 16; ++v) o[x][p][v] = 0.0f;
-        }
-        auto first = [&](int buf, int sub, f32x16 (&acc)[QR]) {
+        auto first = [&](int buf, int sub, f32x16 (&acc)[QR]) __attribute__((always_inline)) {
 #pragma unroll
             for (int x = 0; x < QR; ++x)
 #pragma unroll
@@ -716,45 +846,39 @@ void attention_tile_kernel(const AttnArgs a)
                 for (int x = 0; x < QR; ++x) acc[x] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fk, fq[x][ks], acc[x], 0, 0, 0);
             }
         };
-        auto second = [&](int buf, int sub, int p0, bool whole, bool bad_tile, f32x16 (&acc)[QR]) {
+        auto second = [&](auto masked, int buf, int sub, int p0, f32x16 (&acc)[QR]) __attribute__((always_inline)) {
+            constexpr bool MASKED = decltype(masked)::value;
             bf16x8 fp[QR][2];
 #pragma unroll
             for (int x = 0; x < QR; ++x) {
-                float y[16];
-                uint32_t seen = 0xFFFFu, odd = 0;
+                float z[16];
+                uint32_t seen = 0xFFFFu, odd = 0;            // tokens that the row sees; whose v holds no number
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     f32x4 ks = f32x4{a.scale2, a.scale2, a.scale2, a.scale2};
                     if constexpr (KIND != kCacheBf16) ks = *(const f32x4*)&sks[buf][32 * sub + 8 * j + 4 * half];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) y[4 * j + k] = acc[x][4 * j + k] * ks[k];
+                    for (int k = 0; k < 4; ++k) z[4 * j + k] = __builtin_fmaf(acc[x][4 * j + k], ks[k], sum[x].minus_m);
                 }
-                if (!whole || bad_tile) {
-                    const uint32_t no = sbad[buf][4 * sub + half] | (uint32_t)sbad[buf][4 * sub + 2 + half] << 8;
+                if constexpr (MASKED) {
                     if constexpr (KIND == kCacheBf16) odd = sodd[buf][4 * sub + half] | (uint32_t)sodd[buf][4 * sub + 2 + half] << 8;
 #pragma unroll
                     for (int v = 0; v < 16; ++v) {
                         const int p = p0 + 32 * sub + 8 * (v >> 2) + 4 * half + (v & 3);
-                        if ((no >> v) & 1u) y[v] = nan_f32();
                         if (!(p >= lo[x] && p <= hi[x] && p < end)) {
-                            y[v] = neg_inf();
+                            z[v] = neg_inf();
                             seen &= ~(1u << v);
                         }
                     }
                 }
-                float top = y[0];
+                float top = z[0];
 #pragma unroll
-                for (int v = 1; v < 16; ++v) top = fmaxf(top, y[v]);
-                if (__any(top > m[x] + kRaise)) {
-                    top = fmaxf(top, __shfl_xor(top, 32));
-                    const float up = top > m[x] + kRaise ? top : m[x];
-                    const float fac = up == m[x] ? 1.0f : exp2_fast(m[x] - up);
-                    m[x] = up;
-                    l[x] *= fac;
+                for (int v = 1; v < 16; ++v) top = fmaxf(top, z[v]);
+                row_raise<2>(sum[x], z, top, [&](float by) {
 #pragma unroll
-                    for (int p = 0; p < S::kParts; ++p) o[x][p] *= fac;
-                }
-                const float base = m[x] == neg_inf() ? 0.0f : m[x];
+                    for (int p = 0; p < S::kParts; ++p) o[x][p] *= by;
+                });
+                float p[16];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     f32x4 vs;
@@ -762,17 +886,17 @@ void attention_tile_kernel(const AttnArgs a)
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const int v = 4 * j + k;
-                        float p = exp2_fast(y[v] - base);
-                        l[x] += p;
-                        if constexpr (KIND != kCacheBf16) p *= vs[k];
-                        if (!whole || bad_tile) {
-                            const bool sees = (seen >> v) & 1u;
-                            if (KIND == kCacheBf16 && ((odd >> v) & 1u)) p = nan_f32();
-                            if (!sees) p = 0.0f;
+                        p[v] = exp2_fast(z[v]);
+                        sum[x].l += p[v];
+                        if constexpr (KIND != kCacheBf16) p[v] *= vs[k];
+                        if constexpr (MASKED) {
+                            if (KIND == kCacheBf16 && ((odd >> v) & 1u)) p[v] = nan_f32();
+                            if (!((seen >> v) & 1u)) p[v] = 0.0f;
                         }
-                        fp[x][v >> 3][v & 7] = (__bf16)p;
                     }
                 }
+                fp[x][0] = to_bf16x8(p);
+                fp[x][1] = to_bf16x8(p + 8);
             }
 #pragma unroll
             for (int st = 0; st < 2; ++st)
@@ -783,43 +907,47 @@ void attention_tile_kernel(const AttnArgs a)
                     for (int x = 0; x < QR; ++x) o[x][p] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fv, fp[x][st], o[x][p], 0, 0, 0);
                 }
         };
+        auto products = [&](auto masked, int buf, int p0) __attribute__((always_inline)) {
+            f32x16 acc[2][QR];
+            first(buf, 0, acc[0]);
+#pragma unroll
+            for (int sub = 0; sub < S::kSubs; ++sub) {
+                if (sub + 1 < S::kSubs) first(buf, sub + 1, acc[(sub + 1) & 1]);
+                second(masked, buf, sub, p0, acc[sub & 1]);
+            }
+        };
 
         if (begin < end) {
             load(begin);
             stage(0, begin);
         }
         __syncthreads();
-        int buf = 0;
-        for (int p0 = begin; p0 < end; p0 += S::kTokens, buf ^= 1) {
+        // masked tiles stand at both ends of the part
+        int buf = 0, p0 = begin;
+        auto turn = [&](auto masked) __attribute__((always_inline)) {
             const bool more = p0 + S::kTokens < end;
             if (more) load(p0 + S::kTokens);
-            if (p0 <= some_hi && p0 + S::kTokens > some_lo) {
-                const bool whole = all_lo <= p0 && p0 + S::kTokens - 1 <= all_hi && p0 + S::kTokens <= end;
-                bool bad_tile = false;
-#pragma unroll
-                for (int i = 0; i < 2 * S::kSteps; i += 4) bad_tile |= *(const uint32_t*)&sbad[buf][i] != 0;
-                f32x16 acc[2][QR];
-                first(buf, 0, acc[0]);
-#pragma unroll
-                for (int sub = 0; sub < S::kSubs; ++sub) {
-                    if (sub + 1 < S::kSubs) first(buf, sub + 1, acc[(sub + 1) & 1]);
-                    second(buf, sub, p0, whole, bad_tile, acc[sub & 1]);
-                }
-            }
+            if (!decltype(masked)::value || (p0 <= some_hi && p0 + S::kTokens > some_lo)) products(masked, buf, p0);
             if (more) stage(buf ^ 1, p0 + S::kTokens);
             __syncthreads();
+            p0 += S::kTokens;
+            buf ^= 1;
+        };
+        while (p0 < end) {
+            while (p0 < end && !whole(p0)) turn(std::true_type{});
+            while (p0 < end && whole(p0)) turn(std::false_type{});
         }
 
         // a lane holds, of its rows, units of 8 elements
 #pragma unroll
         for (int x = 0; x < QR; ++x) {
-            l[x] += __shfl_xor(l[x], 32);
+            float l = sum[x].l + __shfl_xor(sum[x].l, 32);
             const int64_t rr = rt * kRows + (wave * QR + x) * 32 + col;
             if (rr >= rows) continue;
             const int64_t i = (int)rr / a.group, t = r.row0 + i;
             const int64_t qh = h * a.group + (rr - i * a.group), at = t * c.heads * a.group + qh;
-            if (hi[x] >= a.s.capacity) l[x] = nan_f32();     // it sees tokens that the table does not hold
-            const float inv = a.splits > 1 ? 1.0f : (l[x] == 0.0f ? 0.0f : 1.0f / l[x]);
+            if (hi[x] >= a.s.capacity) l = nan_f32();     // it sees tokens that the table does not hold
+            const float inv = a.splits > 1 ? 1.0f : (l == 0.0f ? 0.0f : 1.0f / l);
             constexpr int kSlots = 16 / S::kEach;
 #pragma unroll
             for (int k = 0; k < kSlots; ++k) {
@@ -837,8 +965,8 @@ void attention_tile_kernel(const AttnArgs a)
                 }
             }
             if (half == 0) {
-                if (a.splits > 1) *(f32x2*)(a.part_ml + 2 * (at * a.splits + split)) = f32x2{m[x], l[x]};
-                else if (a.lse) a.lse[at] = row_lse(m[x], l[x]);
+                if (a.splits > 1) *(f32x2*)(a.part_ml + 2 * (at * a.splits + split)) = f32x2{sum[x].m(), l};
+                else if (a.lse) a.lse[at] = row_lse(sum[x].m(), l);
             }
         }
     }

@@ -148,12 +148,17 @@ int cache_io(const echo_cache* c, const echo_seqs* s, void* k, int64_t ld_k, voi
 // How a call is split.
 struct AttnPlan {
     bool few, tile;         // which kernels run; with both, a sequence of few rows is the former's
-    int64_t few_tiles, tile_tiles;      // row tiles of a sequence with a block of their own
+    int64_t few_tiles;      // row tiles of a sequence with a block of their own
+    int64_t tile_tiles;     // row tiles of all sequences together, at most
     int splits;             // parts of a row's tokens
     size_t part_ml, total;  // of the workspace: the parts' sums of v, then their m and l
 };
 
-constexpr int64_t kTileRows = 32 * echo::kTileWaves;
+#ifndef TW
+#define TW 4
+#endif
+constexpr int kTileWaves = TW;
+constexpr int64_t kTileRows = 32 * kTileWaves;
 constexpr int64_t kFewBlocks = 4 * kCus, kFewPart = 256, kTileBlocks = 2 * kCus, kTilePart = 512, kMostSplits = 256;
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -166,7 +171,7 @@ AttnPlan attn_plan(const echo_attention_args& p)
     n.tile = most_new * G > echo::kFewRows;
     n.few = !n.tile || p.seqs.seqs > 1;
     n.few_tiles = n.tile ? 1 : ceil_div(most_new * G, echo::kFewRows);
-    n.tile_tiles = ceil_div(most_new * G, kTileRows);
+    n.tile_tiles = T * G / kTileRows + p.seqs.seqs;         // see the kernel's numbering
     // tokens that a row tile sees at most
     int64_t len = std::min(p.seqs.max_len, p.seqs.table_pages * p.cache.page_tokens);
     if (p.window > 0) len = std::min(len, std::min(p.window, len) + ceil_div(n.tile ? kTileRows : echo::kFewRows, G));
@@ -178,7 +183,7 @@ AttnPlan attn_plan(const echo_attention_args& p)
     const int64_t most = std::max<int64_t>(1, (int64_t(1) << 24) / pairs);
     n.splits = (int)std::max<int64_t>(1, std::min(splits, most));
     n.few_tiles = std::max<int64_t>(1, std::min(n.few_tiles, most / n.splits));
-    n.tile_tiles = std::max<int64_t>(1, std::min(n.tile_tiles, most / n.splits));
+    if (n.tile && n.tile_tiles * p.cache.heads * n.splits >= int64_t(1) << 24) n.splits = 1;
     if (n.splits > 1) {
         const int64_t rows = T * p.q_heads;
         n.part_ml = (size_t)(rows * n.splits * p.cache.width * 4);
@@ -204,14 +209,15 @@ int check_attention(const echo_attention_args* p)
 template <int KIND, int DP>
 void attention_go(echo::AttnArgs& a, const AttnPlan& n, hipStream_t st)
 {
-    const bool page16 = a.c.page_tokens % 16 == 0;
+    // 16 tokens of a page at 32-bit offsets from the first
+    const bool page16 = a.c.page_tokens % 16 == 0 && a.c.ld_token < int64_t(1) << 26;
     const int64_t pairs = (int64_t)a.s.seqs * a.c.heads * n.splits;
     a.few_rows = n.few && n.tile ? echo::kFewRows : 0;
     if (n.tile) {
         a.tiles = (uint32_t)n.tile_tiles;
-        const dim3 grid((unsigned)(n.tile_tiles * pairs)), block(64 * echo::kTileWaves);
-        if (page16) hipLaunchKernelGGL((echo::attention_tile_kernel<KIND, DP, 1, true>), grid, block, 0, st, a);
-        else hipLaunchKernelGGL((echo::attention_tile_kernel<KIND, DP, 1, false>), grid, block, 0, st, a);
+        const dim3 grid((unsigned)(n.tile_tiles * a.c.heads * n.splits)), block(64 * kTileWaves);
+        if (page16) hipLaunchKernelGGL((echo::attention_tile_kernel<KIND, DP, kTileWaves, 1, true>), grid, block, 0, st, a);
+        else hipLaunchKernelGGL((echo::attention_tile_kernel<KIND, DP, kTileWaves, 1, false>), grid, block, 0, st, a);
     }
     if (n.few) {
         a.tiles = (uint32_t)n.few_tiles;
