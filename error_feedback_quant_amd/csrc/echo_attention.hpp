@@ -42,12 +42,22 @@ struct AttnArgs {
     int group;              // query heads of a head of the cache
     int causal;
     float scale2;           // scale * log2(e)
-    int splits;             // parts of a row's tokens
-    uint32_t tiles;         // row tiles of a sequence that have a block of their own
     int few_rows;           // rows up to which a sequence is the few-row kernel's, 0: the launched kernel takes all
-    float* part_o;          // [rows][splits][width]
-    float* part_ml;         // [rows][splits][2]
+    uint32_t tiles;         // row tiles: of a sequence (few rows), of the call (many)
+    // parts of a row's tokens and where they leave their sums, for either kernel
+    struct Parts {
+        int splits;
+        float* o;           // [rows][splits][width]
+        float* ml;          // [rows][splits][2]
+    } few, tile;
 };
+
+// A row's number among those that leave parts.  Where both kernels run, the
+// few-row one has few_rows for each sequence and head of the cache.
+__device__ __forceinline__ int64_t few_part(const AttnArgs& a, int64_t at, int b, int h, int64_t row)
+{
+    return a.few_rows ? ((int64_t)b * a.c.heads + h) * a.few_rows + row : at;
+}
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
@@ -59,6 +69,13 @@ __device__ __forceinline__ float nan_f32() { return __builtin_bit_cast(float, 0x
 __device__ __forceinline__ float neg_inf() { return -__builtin_inff(); }
 
 // largest / sum over the lanes that share a query row: lane % 16 with ROWS = 4, lane % 32 with 2
+__device__ __forceinline__ float row_max16(float v)      // within 16 lanes
+{
+    v = fmaxf(v, __builtin_bit_cast(float, dpp_i<0xB1>(__builtin_bit_cast(int, v))));
+    v = fmaxf(v, __builtin_bit_cast(float, dpp_i<0x4E>(__builtin_bit_cast(int, v))));
+    v = fmaxf(v, __builtin_bit_cast(float, dpp_i<0x141>(__builtin_bit_cast(int, v))));
+    return fmaxf(v, __builtin_bit_cast(float, dpp_i<0x140>(__builtin_bit_cast(int, v))));
+}
 template <int ROWS>
 __device__ __forceinline__ float rows_max(float v)
 {
@@ -184,12 +201,32 @@ struct FewTile {
     using S = FewShape<KIND, DP>;
     uint32_t k[2][S::kLoads][S::kKWords];
     uint32_t v[8][S::kPieces][S::kVWords];
-    uint32_t ks[8], vs[8];      // of the lane's 8 tokens
+    uint32_t ks, vs;            // of token lane % 8 among the 8 of the lane's row
 };
+
+// f(0) .. f(7) with the number as a constant
+template <typename F>
+__device__ __forceinline__ void unroll8(F f)
+{
+    using std::integral_constant;
+    f(integral_constant<int, 0>{}); f(integral_constant<int, 1>{}); f(integral_constant<int, 2>{}); f(integral_constant<int, 3>{});
+    f(integral_constant<int, 4>{}); f(integral_constant<int, 5>{}); f(integral_constant<int, 6>{}); f(integral_constant<int, 7>{});
+}
+
+// v of lane E of the octet's lanes (8, or the 16 of a row, of which every
+// eighth holds the same): a broadcast within the row
+template <int UNITS, int E>
+__device__ __forceinline__ uint32_t octet_lane(uint32_t v)
+{
+    const uint32_t a = (uint32_t)dpp_i<0x150 + E>((int)v);   // row_newbcast
+    if constexpr (UNITS >= 16) return a;
+    const uint32_t b = (uint32_t)dpp_i<0x158 + E>((int)v);
+    return threadIdx.x & 8u ? b : a;
+}
 
 // 8 elements of k (words) as bfloat16
 template <int KIND>
-__device__ __forceinline__ bf16x8 k_frag(const uint32_t* w)
+__device__ __forceinline__ bf16x8 k_frag(const uint32_t* w, uint32_t bias)
 {
     u32x4 o;
     if constexpr (KIND == kCacheBf16) {
@@ -199,14 +236,14 @@ __device__ __forceinline__ bf16x8 k_frag(const uint32_t* w)
         for (int i = 0; i < 4; ++i)
             o[i] = upper_pair((float)(int8_t)(w[i / 2] >> (16 * (i & 1))), (float)(int8_t)(w[i / 2] >> (16 * (i & 1) + 8)));
     } else {
-        return codes_bf16(w[0]);
+        return codes_bf16(w[0], bias);
     }
     return __builtin_bit_cast(bf16x8, o);
 }
 
 // element f of 8 tokens' pieces of v
 template <int KIND, int WORDS>
-__device__ __forceinline__ bf16x8 v_frag(const uint32_t (*v)[WORDS], int f)
+__device__ __forceinline__ bf16x8 v_frag(const uint32_t (*v)[WORDS], int f, uint32_t bias)
 {
     u32x4 o;
 #pragma unroll
@@ -219,7 +256,7 @@ __device__ __forceinline__ bf16x8 v_frag(const uint32_t (*v)[WORDS], int f)
         } else {
             const uint32_t h = __builtin_amdgcn_perm(v[2 * i + 1][0], v[2 * i][0], f < 4 ? 0x05040100u : 0x07060302u);
             const int at = 4 * (f & 3);
-            o[i] = ((at ? h >> (at - 3) : h << 3) & 0x00780078u) | 0x41804180u;
+            o[i] = ((at ? h >> (at - 3) : h << 3) & 0x00780078u) | bias;
         }
     }
     return __builtin_bit_cast(bf16x8, o);
@@ -232,16 +269,13 @@ __device__ __forceinline__ uint32_t not_finite2(uint32_t w)
     return m | ((w & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u);
 }
 
-// waves on a SIMD that the registers of two tiles leave room for
-constexpr int few_waves(int kind, int dp)
-{
-    return dp == 64 ? (kind == kCacheI4 ? 4 : 3) : (dp == 128 ? (kind == kCacheI4 ? 3 : 2) : (kind == kCacheBf16 ? 1 : 2));
-}
+// waves on a SIMD that a tile's and the sums' registers leave room for
+constexpr int few_waves(int dp) { return dp == 64 ? 4 : (dp == 128 ? 3 : 2); }
 
 // PAGE16: pages are a multiple of 16 tokens, so the 16 tokens of a tile's half
 // lie in one page; otherwise every lane looks its tokens up.
 template <int KIND, int DP, bool PAGE16>
-__global__ __launch_bounds__(64 * kFewAttnWaves) __attribute__((amdgpu_waves_per_eu(few_waves(KIND, DP))))
+__global__ __launch_bounds__(64 * kFewAttnWaves) __attribute__((amdgpu_waves_per_eu(few_waves(DP))))
 void attention_few_kernel(const AttnArgs a)
 {
     using S = FewShape<KIND, DP>;
@@ -253,12 +287,13 @@ void attention_few_kernel(const AttnArgs a)
     const CacheView& c = a.c;
     const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int col = lane & 15, g = lane >> 4;
-    uint32_t id = blockIdx.x;
-    const int split = id % (uint32_t)a.splits;
-    id /= (uint32_t)a.splits;
+    // the row tiles of a part are 8 blocks apart: they share an XCD's cache
+    uint32_t id = blockIdx.x / 8 / a.tiles * 8 + blockIdx.x % 8;
+    const int split = id % (uint32_t)a.few.splits;
+    id /= (uint32_t)a.few.splits;
     const int h = id % (uint32_t)c.heads;
-    id /= (uint32_t)c.heads;
-    const int b = id % (uint32_t)a.s.seqs;
+    const int b = id / (uint32_t)c.heads;
+    if (b >= a.s.seqs) return;
     const RowSpan r = seq_span(a.s, b);
     const int rows = r.n * a.group;                      // below 2^31 with all heads
     if (a.few_rows && rows > a.few_rows) return;         // the other kernel's
@@ -268,7 +303,7 @@ void attention_few_kernel(const AttnArgs a)
     const uint32_t koff = (uint32_t)(col * token_bytes + cache_bytes<KIND>(S::kE * g));      // for PAGE16, whose host check
     const uint32_t voff = (uint32_t)(4 * g * token_bytes + cache_bytes<KIND>(S::kVE * col)); // keeps them in 32 bits
 
-    for (int64_t rt = id / (uint32_t)a.s.seqs; rt * kFewRows < rows; rt += a.tiles) {
+    for (int64_t rt = blockIdx.x / 8 % a.tiles; rt * kFewRows < rows; rt += a.tiles) {
         // this lane's row
         const int64_t rr = rt * kFewRows + col;
         const bool there = rr < rows;
@@ -280,7 +315,7 @@ void attention_few_kernel(const AttnArgs a)
         const int lo = a.window ? pos - a.window + 1 : 0;
         int begin, end;
         seen_span(a, r, (int)rt * kFewRows / a.group, ((int)min((int64_t)rows, (rt + 1) * kFewRows) - 1) / a.group, begin, end);
-        split_span(a.splits, split, begin, end);
+        split_span(a.few.splits, split, begin, end);
 
         // q as the second operand, in the order of k's elements
         bf16x8 fq[kSteps];
@@ -341,6 +376,7 @@ void attention_few_kernel(const AttnArgs a)
         constexpr int kPieceBytes = 16 * S::kVBytes;
         auto load = [&](FewTile<KIND, DP>& f, int p0, const Pages& pg) __attribute__((always_inline)) {
             uint32_t kbad = 0, bad = 0;                      // tokens without a place, by bits: their scores are NaN
+            int64_t mine = 0;                                // entry of token lane % 8's scales
             if constexpr (PAGE16) {
                 // a base for 16 tokens in scalar registers, and the lane's offsets
 #pragma unroll
@@ -359,10 +395,10 @@ void attention_few_kernel(const AttnArgs a)
                         for (int p = 0; p < S::kPieces; ++p) take_v(f.v[4 * u + e][p], vr + e * token_bytes + p * kPieceBytes + voff, p);
                     if constexpr (KIND != kCacheBf16) {
                         const int64_t sr = at * c.ld_sp + h * c.ld_sh + slot;
-                        __builtin_memcpy(&f.ks[4 * u], (const uint8_t*)(c.ks + sr) + 16u * g, 16);
-                        __builtin_memcpy(&f.vs[4 * u], (const uint8_t*)(c.vs + sr) + 16u * g, 16);
+                        mine = u == 0 || (lane & 4u) ? sr : mine;
                     }
                 }
+                mine += 4 * g + (lane & 3u);
             } else {
                 auto place = [&](int t, int32_t page, int64_t& o, int64_t& s) __attribute__((always_inline)) {
                     const uint32_t slot = (uint32_t)min(t, end - 1) % c.page_tokens;
@@ -383,16 +419,15 @@ void attention_few_kernel(const AttnArgs a)
                     if (place(p0 + 16 * (e / 4) + 4 * g + (e & 3), pg.n[e], o, s)) bad |= 1u << e;
 #pragma unroll
                     for (int p = 0; p < S::kPieces; ++p) take_v(f.v[e][p], vb + cache_bytes<KIND>(o + 128 * p + S::kVE * col), p);
-                    if constexpr (KIND != kCacheBf16) {
-                        f.ks[e] = c.ks[s];
-                        f.vs[e] = c.vs[s];
-                    }
+                    mine = (int)(lane & 7u) == e ? s : mine;
                 }
             }
+            if constexpr (KIND != kCacheBf16) {
+                f.ks = c.ks[mine];
+                f.vs = c.vs[mine];
+            }
             if (__any((bad | kbad) != 0)) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (KIND != kCacheBf16 && (bad >> e) & 1u) f.ks[e] = KIND == kCacheI8 ? 0x7FC00000u : 0x7E00u;
+                if (KIND != kCacheBf16 && (bad >> (lane & 7u)) & 1u) f.ks = KIND == kCacheI8 ? 0x7FC00000u : 0x7E00u;
 #pragma unroll
                 for (int u = 0; u < 2; ++u)
                     if (KIND == kCacheBf16 && (kbad >> u) & 1u) f.k[u][0][0] = 0x7FC07FC0u;
@@ -404,40 +439,44 @@ void attention_few_kernel(const AttnArgs a)
         for (int f = 0; f < kFrags; ++f) o[f] = f32x4{0, 0, 0, 0};
         int p0 = begin + kFewTile * (int)wave;
         RowSum sum;
-        float off = 0.0f;                                    // what the codes' offsets add to every element
+        float off = 0.0f, off16 = 0.0f;                      // what zero points and 1/16 of the offset add to every element
+        uint32_t bias = 0x41804180u;                         // two 16.0: in a register, an and-or takes one literal
+        asm("" : "+v"(bias));
 
         auto take = [&](FewTile<KIND, DP>& f) __attribute__((always_inline)) {
             f32x4 acc[2];
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                acc[u] = f32x4{0, 0, 0, 0};
+                // the offset 16 of 4-bit codes is off from the start
+                const float first = KIND == kCacheI4 ? -16.0f * qsum : 0.0f;
+                acc[u] = f32x4{first, first, first, first};
 #pragma unroll
                 for (int st = 0; st < kSteps; ++st) {
                     constexpr int kPer = S::kE / 8, kW = S::kKWords / kPer;
-                    acc[u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k_frag<KIND>(&f.k[u][st / kPer][kW * (st % kPer)]),
+                    acc[u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k_frag<KIND>(&f.k[u][st / kPer][kW * (st % kPer)], bias),
                                                                      fq[st], acc[u], 0, 0, 0);
                 }
             }
             float z[8];
+            uint32_t ks[8], vs[8];
+            if constexpr (KIND != kCacheBf16)
+                unroll8([&](auto e) {
+                    ks[e] = octet_lane<16, e>(f.ks);
+                    vs[e] = octet_lane<16, e>(f.vs);
+                });
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const float s = acc[e / 4][e % 4];
                 if constexpr (KIND == kCacheBf16) z[e] = __builtin_fmaf(s, a.scale2, sum.minus_m);
-                else if constexpr (KIND == kCacheI8) z[e] = __builtin_fmaf(s, __builtin_bit_cast(float, f.ks[e]) * a.scale2, sum.minus_m);
-                else z[e] = __builtin_fmaf(__builtin_fmaf(-(16.0f + half_hi(f.ks[e])), qsum, s), half_lo(f.ks[e]) * a.scale2, sum.minus_m);
+                else if constexpr (KIND == kCacheI8) z[e] = __builtin_fmaf(s * a.scale2, __builtin_bit_cast(float, ks[e]), sum.minus_m);
+                else z[e] = __builtin_fmaf(__builtin_fmaf(half_hi(ks[e]), -qsum, s) * a.scale2, half_lo(ks[e]), sum.minus_m);
             }
-            // The mask costs every tile three instructions a score; tiles of two
-            // kinds would cost the registers of another tile on its way.
-            const uint32_t from = lo - p0 - 4 * g, span = min(hi, end - 1) - lo;     // a row that sees nothing has a span below -1
-            bool sees[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                sees[e] = 16u * (e / 4) + (e & 3) - from <= span && (int)span >= 0;
-                z[e] = sees[e] ? z[e] : neg_inf();
-            }
-            uint32_t odd = 0;                                // tokens whose v holds no number
-            if constexpr (KIND == kCacheBf16) {
-                if (!(__all(!there || (lo <= p0 && p0 + kFewTile - 1 <= hi)) && p0 + kFewTile <= end)) {
+            // Tiles that are masked in part: the weight is 0 for a score of
+            // -infinity, and so has what it is multiplied with to be a number.
+            if (!(__all(!there || (lo <= p0 && p0 + kFewTile - 1 <= hi)) && p0 + kFewTile <= end)) {
+                asm volatile("");                            // a branch, not selects in every tile
+                uint32_t odd = 0;                            // tokens whose v holds no number
+                if constexpr (KIND == kCacheBf16) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
 #pragma unroll
@@ -450,12 +489,21 @@ void attention_few_kernel(const AttnArgs a)
                             }
                     odd = group_fold<16>(odd, [](uint32_t p, uint32_t q) { return p | q; });
                 }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int p = p0 + 16 * (e / 4) + 4 * g + (e & 3);
+                    const bool sees = (p >= lo) & (p <= hi) & (p < end);
+                    if (KIND == kCacheBf16 && ((odd >> e) & 1u)) z[e] = nan_f32();
+                    z[e] = sees ? z[e] : neg_inf();
+                    if constexpr (KIND != kCacheBf16) vs[e] = sees ? vs[e] : 0u;     // of this row and token
+                }
             }
             float top = z[0];
 #pragma unroll
             for (int e = 1; e < 8; ++e) top = fmaxf(top, z[e]);
             row_raise<4>(sum, z, top, [&](float by) {
                 off *= by;
+                off16 *= by;
 #pragma unroll
                 for (int j = 0; j < kFrags; ++j) o[j] *= by;
             });
@@ -464,16 +512,17 @@ void attention_few_kernel(const AttnArgs a)
             for (int e = 0; e < 8; ++e) {
                 p[e] = exp2_fast(z[e]);
                 sum.l += p[e];
-                if constexpr (KIND == kCacheI8) p[e] *= __builtin_bit_cast(float, f.vs[e]);
-                if constexpr (KIND == kCacheI4) p[e] *= half_lo(f.vs[e]);
-                if (KIND == kCacheBf16 && ((odd >> e) & 1u)) p[e] = nan_f32();
-                p[e] = sees[e] ? p[e] : 0.0f;
+                if constexpr (KIND == kCacheI8) p[e] *= __builtin_bit_cast(float, vs[e]);
+                if constexpr (KIND == kCacheI4) p[e] = __builtin_fmaf(p[e], half_lo(vs[e]), 0.0f);
             }
             const bf16x8 fp = to_bf16x8(p);
             if constexpr (KIND == kCacheI4) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    off = __builtin_fmaf((float)fp[e], sees[e] ? 16.0f + half_hi(f.vs[e]) : 0.0f, off);
+                for (int e = 0; e < 8; ++e) {
+                    const float w = (float)fp[e];
+                    off = __builtin_fmaf(w, half_hi(vs[e]), off);
+                    off16 += w;
+                }
             }
 #pragma unroll
             for (int pc = 0; pc < S::kPieces; ++pc) {
@@ -484,39 +533,27 @@ void attention_few_kernel(const AttnArgs a)
                     for (int w = 0; w < S::kVWords; ++w) v[e][w] = f.v[e][pc][w];
 #pragma unroll
                 for (int j = 0; j < S::kVE; ++j)
-                    o[S::kVE * pc + j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v_frag<KIND, S::kVWords>(v, j), fp,
+                    o[S::kVE * pc + j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v_frag<KIND, S::kVWords>(v, j, bias), fp,
                                                                                o[S::kVE * pc + j], 0, 0, 0);
             }
         };
+        // Other waves cover a wave's wait for its tile: three on a SIMD that load
+        // and multiply in turn read 3.9 TB/s (64 tokens over up to 16384 in 4
+        // bits, 172 us), two or three with their next tile on its way 3.8 and 3.2.
         constexpr int kStep = kFewTile * kFewAttnWaves;
-        constexpr bool kAhead = DP < 256;                    // the next tile is on its way while one is multiplied
         if (p0 < end) {
-            FewTile<KIND, DP> f;
             Pages pg = lookup(p0);
-            if constexpr (kAhead) {
+            for (; p0 < end; p0 += kStep) {
+                FewTile<KIND, DP> f;
                 load(f, p0, pg);
                 pg = lookup(p0 + kStep);
-                while (p0 + kStep < end) {
-                    FewTile<KIND, DP> next;
-                    load(next, p0 + kStep, pg);
-                    pg = lookup(p0 + 2 * kStep);
-                    take(f);
-                    p0 += kStep;
-                    f = next;
-                }
                 take(f);
-            } else {
-                for (; p0 < end; p0 += kStep) {
-                    load(f, p0, pg);
-                    pg = lookup(p0 + kStep);
-                    take(f);
-                }
             }
         }
 
         // the waves' sums to the largest m
         const float m = sum.m(), l = rows4_sum(sum.l);
-        if constexpr (KIND == kCacheI4) off = rows4_sum(off);
+        if constexpr (KIND == kCacheI4) off = rows4_sum(__builtin_fmaf(16.0f, off16, off));
         if (g == 0) {
             sm[wave][col] = m;
             sl[wave][col] = l;
@@ -558,11 +595,12 @@ void attention_few_kernel(const AttnArgs a)
             const int64_t at = t2 * c.heads * a.group + h * a.group + (row - i2 * a.group);
             const int last = a.causal ? r.pos(i2) : r.len - 1;
             if (last >= a.s.capacity) ll = nan_f32();        // it sees tokens that the table does not hold
-            if (a.splits > 1) {
-                float* po = a.part_o + (at * a.splits + split) * c.width + d;
+            if (a.few.splits > 1) {
+                const int64_t part = few_part(a, at, b, h, row) * a.few.splits + split;
+                float* po = a.few.o + part * c.width + d;
                 *(f32x4*)po = f32x4{e[0], e[1], e[2], e[3]};
                 *(f32x4*)(po + 4) = f32x4{e[4], e[5], e[6], e[7]};
-                if (d == 0) *(f32x2*)(a.part_ml + 2 * (at * a.splits + split)) = f32x2{mm, ll};
+                if (d == 0) *(f32x2*)(a.few.ml + 2 * part) = f32x2{mm, ll};
             } else {
                 const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
 #pragma unroll
@@ -599,27 +637,6 @@ struct TileShape {
     static constexpr int kParts = DP / 32;               // 32 elements: the rows of a second one
     static constexpr int kEach = 32 / kUnits;            // elements of a unit in a part
 };
-
-// f(0) .. f(7) with the number as a constant
-template <typename F>
-__device__ __forceinline__ void unroll8(F f)
-{
-    using std::integral_constant;
-    f(integral_constant<int, 0>{}); f(integral_constant<int, 1>{}); f(integral_constant<int, 2>{}); f(integral_constant<int, 3>{});
-    f(integral_constant<int, 4>{}); f(integral_constant<int, 5>{}); f(integral_constant<int, 6>{}); f(integral_constant<int, 7>{});
-}
-
-// v of lane E of the octet's lanes (8, or the 16 of a row, of which every
-// eighth holds the same): a broadcast within the row
-template <int UNITS, int E>
-__device__ __forceinline__ float octet_lane(float v)
-{
-    const int i = __builtin_bit_cast(int, v);
-    const int a = dpp_i<0x150 + E>(i);                       // row_newbcast
-    if constexpr (UNITS >= 16) return __builtin_bit_cast(float, a);
-    const int b = dpp_i<0x158 + E>(i);
-    return __builtin_bit_cast(float, threadIdx.x & 8u ? b : a);
-}
 
 template <int KIND>
 struct RawUnit {                                         // 8 elements as they lie in the cache
@@ -715,7 +732,7 @@ void attention_tile_kernel(const AttnArgs a)
         int begin, end;
         const int i0 = (int)(rt * kRows) / a.group, i1 = ((int)min((int64_t)rows, (rt + 1) * kRows) - 1) / a.group;
         seen_span(a, r, i0, i1, begin, end);
-        split_span(a.splits, split, begin, end);
+        split_span(a.tile.splits, split, begin, end);
         // tiles inside these bounds are seen whole by every row of the block
         const int block_hi = min(a.causal ? r.pos(i0) : r.len - 1, end - 1);
         const int block_lo = a.window ? r.pos(i1) - a.window + 1 : 0;
@@ -765,8 +782,7 @@ void attention_tile_kernel(const AttnArgs a)
         auto stage = [&](int buf, int p0) __attribute__((always_inline)) {
             float z[8];                                      // zero points
             if constexpr (KIND == kCacheI4) {
-                const float mine = half_hi(word);
-                unroll8([&](auto e) { z[e] = octet_lane<S::kUnits, e>(mine); });
+                unroll8([&](auto e) { z[e] = half_hi(octet_lane<S::kUnits, e>(word)); });
             } else {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) z[e] = 0.0f;
@@ -947,7 +963,7 @@ void attention_tile_kernel(const AttnArgs a)
             const int64_t i = (int)rr / a.group, t = r.row0 + i;
             const int64_t qh = h * a.group + (rr - i * a.group), at = t * c.heads * a.group + qh;
             if (hi[x] >= a.s.capacity) l = nan_f32();     // it sees tokens that the table does not hold
-            const float inv = a.splits > 1 ? 1.0f : (l == 0.0f ? 0.0f : 1.0f / l);
+            const float inv = a.tile.splits > 1 ? 1.0f : (l == 0.0f ? 0.0f : 1.0f / l);
             constexpr int kSlots = 16 / S::kEach;
 #pragma unroll
             for (int k = 0; k < kSlots; ++k) {
@@ -956,8 +972,8 @@ void attention_tile_kernel(const AttnArgs a)
                 float e[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) e[j] = o[x][j / S::kEach][k + kSlots * (j % S::kEach)] * inv;
-                if (a.splits > 1) {
-                    float* po = a.part_o + (at * a.splits + split) * c.width + d;
+                if (a.tile.splits > 1) {
+                    float* po = a.tile.o + (at * a.tile.splits + split) * c.width + d;
                     *(f32x4*)po = f32x4{e[0], e[1], e[2], e[3]};
                     *(f32x4*)(po + 4) = f32x4{e[4], e[5], e[6], e[7]};
                 } else {
@@ -965,46 +981,77 @@ void attention_tile_kernel(const AttnArgs a)
                 }
             }
             if (half == 0) {
-                if (a.splits > 1) *(f32x2*)(a.part_ml + 2 * (at * a.splits + split)) = f32x2{sum[x].m(), l};
+                if (a.tile.splits > 1) *(f32x2*)(a.tile.ml + 2 * (at * a.tile.splits + split)) = f32x2{sum[x].m(), l};
                 else if (a.lse) a.lse[at] = row_lse(sum[x].m(), l);
             }
         }
     }
 }
 
-// Joins the parts of every row, in the order of the parts: a wave to a row, 4
-// elements of it to a lane.
+// Joins the parts of every row, in a fixed order: a wave to a row, whose lanes
+// first take a part each for the common m and the parts' factors; then half a
+// wave takes every other part, with kAhead loads on their way.  4 or 8 elements
+// to a lane.
+template <int DP>
 __global__ __launch_bounds__(kBlock) void attention_join_kernel(const AttnArgs a, int64_t rows)
 {
+    constexpr int kE = DP <= 128 ? 4 : 8, kAhead = 4;
     const CacheView& c = a.c;
-    const int lane = threadIdx.x & 63;
+    const int lane = threadIdx.x & 63, half = lane >> 5, d = kE * (lane & 31);
     const int heads = c.heads * a.group;
-    for (int64_t at = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); at < rows; at += (int64_t)gridDim.x * 4) {
+    for (int64_t at = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); at < rows; at += (int64_t)gridDim.x * 4) {
         const int64_t t = at / heads;
-        if (seq_of_row(a.s, t) < 0) continue;
-        const float* ml = a.part_ml + 2 * at * a.splits;
-        float m = neg_inf();
-        for (int s = 0; s < a.splits; ++s) m = fmaxf(m, ml[2 * s]);
-        float l = 0.0f;
-        f32x4 o = {0, 0, 0, 0};
-        for (int s = 0; s < a.splits; ++s) {
-            const float ms = ml[2 * s], ls = ml[2 * s + 1];
-            if (ls == 0.0f) continue;
-            const float f = ms == neg_inf() ? ls : exp2_fast(ms - m);          // m of -inf: l is NaN
-            l = __builtin_fmaf(ls, f, l);
-            if (4 * lane < c.width) {
-                const f32x4 v = *(const f32x4*)(a.part_o + (at * a.splits + s) * c.width + 4 * lane);
+        const int qh = (int)(at - t * heads);
+        const int b = seq_of_row(a.s, t);
+        if (b < 0) continue;
+        const int64_t row0 = a.s.starts[b], n = (int64_t)a.s.starts[b + 1] - row0;
+        const bool is_few = a.tile.splits == 0 || (a.few_rows && n * a.group <= a.few_rows);
+        const AttnArgs::Parts& p = is_few ? a.few : a.tile;
+        const int splits = p.splits;
+        if (splits <= 1) continue;                           // written by its kernel
+        const int h = qh / a.group;
+        const int64_t part = (is_few ? few_part(a, at, b, h, (t - row0) * a.group + (qh - h * a.group)) : at) * splits;
+        const float* ml = p.ml + 2 * part;
+        const float* po = p.o + part * c.width + d;
+        // the parts' m, and their l at the common m; at most 64 parts
+        float m = neg_inf(), l = 0.0f;
+        if (lane < splits) {
+            const f32x2 v = *(const f32x2*)(ml + 2 * lane);
+            m = v.x;
+            l = v.y;
+        }
+        const float top = rows_max<4>(row_max16(m));
+        const float f = l == 0.0f ? 0.0f : (m == neg_inf() ? l : exp2_fast(m - top));     // m of -inf: l is NaN
+        const float sum = wave_sum(l * f);
+        float o[kE] = {};
+        const bool in = d < c.width;
+        for (int s0 = 0; s0 < splits; s0 += 2 * kAhead) {
+            f32x4 v[kAhead][kE / 4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) o[k] = __builtin_fmaf(v[k], f, o[k]);
+            for (int i = 0; i < kAhead; ++i) {
+                const int s = min(s0 + 2 * i + half, splits - 1);
+#pragma unroll
+                for (int k = 0; k < kE / 4; ++k) v[i][k] = in ? *(const f32x4*)(po + (int64_t)s * c.width + 4 * k) : f32x4{0, 0, 0, 0};
+            }
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                const int s = s0 + 2 * i + half;
+                const float fs = __shfl(f, min(s, splits - 1));
+                if (s < splits && fs != 0.0f) {
+#pragma unroll
+                    for (int k = 0; k < kE; ++k) o[k] = __builtin_fmaf(v[i][k / 4][k % 4], fs, o[k]);
+                }
             }
         }
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-        if (4 * lane < c.width) {
-            const bf16x2 w[2] = {bf16x2{(__bf16)(o[0] * inv), (__bf16)(o[1] * inv)},
-                                 bf16x2{(__bf16)(o[2] * inv), (__bf16)(o[3] * inv)}};
-            __builtin_memcpy(a.out + t * a.ld_out + (at - t * heads) * c.width + 4 * lane, w, 8);
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        uint32_t w[kE / 2];
+#pragma unroll
+        for (int k = 0; k < kE; k += 2) {
+            const float x = (o[k] + __shfl_xor(o[k], 32)) * inv, y = (o[k + 1] + __shfl_xor(o[k + 1], 32)) * inv;
+            w[k / 2] = __builtin_bit_cast(uint32_t, bf16x2{(__bf16)x, (__bf16)y});
         }
-        if (lane == 0 && a.lse) a.lse[at] = row_lse(m, l);
+        if (half == 0 && in) __builtin_memcpy(a.out + t * a.ld_out + (int64_t)qh * c.width + d, w, sizeof(w));
+        if (lane == 0 && a.lse) a.lse[at] = row_lse(top, sum);
     }
 }
 

@@ -149,45 +149,65 @@ int cache_io(const echo_cache* c, const echo_seqs* s, void* k, int64_t ld_k, voi
 struct AttnPlan {
     bool few, tile;         // which kernels run; with both, a sequence of few rows is the former's
     int64_t few_tiles;      // row tiles of a sequence with a block of their own
+    int tile_waves;         // of a block of the other kernel, 32 rows each
     int64_t tile_tiles;     // row tiles of all sequences together, at most
-    int splits;             // parts of a row's tokens
-    size_t part_ml, total;  // of the workspace: the parts' sums of v, then their m and l
+    int few_splits, tile_splits;        // parts of a row's tokens
+    size_t few_ml, tile_o, tile_ml, total;      // of the workspace: the parts' sums of v, and their m and l
 };
 
-#ifndef TW
-#define TW 4
-#endif
-constexpr int kTileWaves = TW;
-constexpr int64_t kTileRows = 32 * kTileWaves;
-constexpr int64_t kFewBlocks = 4 * kCus, kFewPart = 256, kTileBlocks = 2 * kCus, kTilePart = 512, kMostSplits = 256;
+constexpr int64_t kFewAlone = 64, kFewBeside = 16;
+constexpr int64_t kFewBlocks = 8 * kCus, kFewBesideBlocks = 4 * kCus, kFewPart = 256, kTileBlocks = 2 * kCus, kTilePart = 512, kMostSplits = 64;
+constexpr int64_t kMostBlocks = int64_t(1) << 22;       // their threads are 32 bits
+
+constexpr int64_t kMaxQueries = int64_t(1) << 29;
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Parts of `len` tokens so that `blocks` become `want`, none shorter than `part`.
+int64_t splits_for(int64_t blocks, int64_t want, int64_t len, int64_t part)
+{
+    const int64_t s = std::min({ceil_div(want, std::max<int64_t>(1, blocks)), ceil_div(len, part), kMostSplits});
+    return std::max<int64_t>(1, std::min(s, kMostBlocks / std::max<int64_t>(1, blocks)));
+}
+
+// 16 tokens of a page together, at 32-bit offsets from the first
+bool paged16(const echo_cache& c) { return c.page_tokens % 16 == 0 && c.ld_token < int64_t(1) << 26; }
 
 AttnPlan attn_plan(const echo_attention_args& p)
 {
     AttnPlan n = {};
-    const int64_t G = p.q_heads / p.cache.heads, T = p.seqs.tokens, pairs = p.seqs.seqs * p.cache.heads;
+    const int64_t G = p.q_heads / p.cache.heads, T = p.seqs.tokens, H = p.cache.heads, pairs = p.seqs.seqs * H;
     const int64_t most_new = std::max<int64_t>(1, std::min(p.seqs.max_new, T));
-    n.tile = most_new * G > echo::kFewRows;
+    n.tile = most_new * G > kFewAlone;
     n.few = !n.tile || p.seqs.seqs > 1;
-    n.few_tiles = n.tile ? 1 : ceil_div(most_new * G, echo::kFewRows);
-    n.tile_tiles = T * G / kTileRows + p.seqs.seqs;         // see the kernel's numbering
     // tokens that a row tile sees at most
     int64_t len = std::min(p.seqs.max_len, p.seqs.table_pages * p.cache.page_tokens);
-    if (p.window > 0) len = std::min(len, std::min(p.window, len) + ceil_div(n.tile ? kTileRows : echo::kFewRows, G));
-    // blocks that have work, as far as the host can tell
-    const int64_t blocks = n.tile ? std::max<int64_t>(1, T * G / kTileRows) * p.cache.heads : n.few_tiles * pairs;
-    int64_t splits = ceil_div(n.tile ? kTileBlocks : kFewBlocks, blocks);
-    splits = std::min(splits, std::min(ceil_div(len, n.tile ? kTilePart : kFewPart), kMostSplits));
-    // a launch's blocks are 32 bits: the kernels stride over the row tiles
-    const int64_t most = std::max<int64_t>(1, (int64_t(1) << 24) / pairs);
-    n.splits = (int)std::max<int64_t>(1, std::min(splits, most));
-    n.few_tiles = std::max<int64_t>(1, std::min(n.few_tiles, most / n.splits));
-    if (n.tile && n.tile_tiles * p.cache.heads * n.splits >= int64_t(1) << 24) n.splits = 1;
-    if (n.splits > 1) {
-        const int64_t rows = T * p.q_heads;
-        n.part_ml = (size_t)(rows * n.splits * p.cache.width * 4);
-        n.total = n.part_ml + (size_t)(rows * n.splits * 8);
+    const int64_t seen = p.window > 0 ? std::min(p.window, len) : len;
+    auto part = [&](int64_t rows, int64_t splits, size_t& o, size_t& ml) {
+        if (splits <= 1) return;
+        o = (n.total + 255) & ~(size_t)255;
+        ml = o + (size_t)(rows * splits * p.cache.width * 4);
+        n.total = ml + (size_t)(rows * splits * 8);
+    };
+    if (n.few) {
+        n.few_tiles = std::max<int64_t>(1, std::min(ceil_div(n.tile ? kFewBeside : most_new * G, echo::kFewRows), kMostBlocks / pairs));
+        const int64_t blocks = n.few_tiles * pairs;
+        n.few_splits = (int)splits_for(blocks, n.tile ? kFewBesideBlocks : kFewBlocks, std::min(len, seen + echo::kFewRows / G + 1), kFewPart);
+        size_t first = 0;
+        part(n.tile ? pairs * kFewBeside : T * p.q_heads, n.few_splits, first, n.few_ml);
+    }
+    if (n.tile) {
+        // Eight waves share what they stage, where there are blocks for all CUs
+        // several times over (8192 tokens over 8192, 8 bits: 673 us with four
+        // waves, 615 with eight; 512 tokens beside 7 sequences: 170 and 177).
+        n.tile_waves = paged16(p.cache) && p.cache.width <= 128 && T * G * H >= 256 * 4 * kCus ? 8 : 4;
+        const int64_t tile_rows = 32 * n.tile_waves;
+        n.tile_tiles = T * G / tile_rows + p.seqs.seqs;     // see the kernel's numbering
+        // those that have work, as far as the host can tell
+        n.tile_splits = (int)splits_for(std::max<int64_t>(1, T * G / tile_rows) * H, kTileBlocks,
+                                        std::min(len, seen + tile_rows / G + 1), kTilePart);
+        if (n.tile_tiles * H * n.tile_splits > kMostBlocks) n.tile_splits = 1;
+        part(T * p.q_heads, n.tile_splits, n.tile_o, n.tile_ml);
     }
     return n;
 }
@@ -199,7 +219,7 @@ int check_attention(const echo_attention_args* p)
     if (rc) return rc;
     if ((rc = check_seqs(p->seqs))) return rc;
     if (p->q_heads < 1 || p->q_heads % p->cache.heads || p->q_heads > kMaxRows) return ECHO_ESHAPE;
-    if (p->seqs.tokens * p->q_heads > kMaxRows || p->seqs.seqs * p->cache.heads > (int64_t(1) << 24)) return ECHO_ESHAPE;
+    if (p->seqs.tokens * p->q_heads > kMaxQueries || p->seqs.seqs * p->cache.heads > kMostBlocks) return ECHO_ESHAPE;
     const int64_t row = p->q_heads * p->cache.width;
     if (bad_ld(p->ld_q, p->seqs.tokens, row) || bad_ld(p->ld_out, p->seqs.tokens, row)) return ECHO_ESHAPE;
     if (p->window < 0 || (p->causal != 0 && p->causal != 1) || !std::isfinite(p->scale)) return ECHO_EINVAL;
@@ -207,32 +227,41 @@ int check_attention(const echo_attention_args* p)
 }
 
 template <int KIND, int DP>
-void attention_go(echo::AttnArgs& a, const AttnPlan& n, hipStream_t st)
+void attention_go(echo::AttnArgs& a, const AttnPlan& n, bool page16, hipStream_t st)
 {
-    // 16 tokens of a page at 32-bit offsets from the first
-    const bool page16 = a.c.page_tokens % 16 == 0 && a.c.ld_token < int64_t(1) << 26;
-    const int64_t pairs = (int64_t)a.s.seqs * a.c.heads * n.splits;
-    a.few_rows = n.few && n.tile ? echo::kFewRows : 0;
+    const int64_t pairs = (int64_t)a.s.seqs * a.c.heads;
     if (n.tile) {
         a.tiles = (uint32_t)n.tile_tiles;
-        const dim3 grid((unsigned)(n.tile_tiles * a.c.heads * n.splits)), block(64 * kTileWaves);
-        if (page16) hipLaunchKernelGGL((echo::attention_tile_kernel<KIND, DP, kTileWaves, 1, true>), grid, block, 0, st, a);
-        else hipLaunchKernelGGL((echo::attention_tile_kernel<KIND, DP, kTileWaves, 1, false>), grid, block, 0, st, a);
+        const dim3 grid((unsigned)(n.tile_tiles * a.c.heads * n.tile_splits)), block(64 * n.tile_waves);
+        if (!page16) {
+            hipLaunchKernelGGL((echo::attention_tile_kernel<KIND, DP, 4, 1, false>), grid, block, 0, st, a);
+        } else if (n.tile_waves == 4) {
+            hipLaunchKernelGGL((echo::attention_tile_kernel<KIND, DP, 4, 1, true>), grid, block, 0, st, a);
+        } else if constexpr (DP < 256) {
+            hipLaunchKernelGGL((echo::attention_tile_kernel<KIND, DP, 8, 1, true>), grid, block, 0, st, a);
+        }
     }
     if (n.few) {
         a.tiles = (uint32_t)n.few_tiles;
-        const dim3 grid((unsigned)(n.few_tiles * pairs)), block(64 * echo::kFewAttnWaves);
+        const dim3 grid((unsigned)(n.few_tiles * ceil_div(pairs * n.few_splits, 8) * 8)), block(64 * echo::kFewAttnWaves);
         if (page16) hipLaunchKernelGGL((echo::attention_few_kernel<KIND, DP, true>), grid, block, 0, st, a);
         else hipLaunchKernelGGL((echo::attention_few_kernel<KIND, DP, false>), grid, block, 0, st, a);
     }
 }
 
-template <int KIND>
-void attention_sized(echo::AttnArgs& a, const AttnPlan& n, hipStream_t st)
+void attention_join(const echo::AttnArgs& a, int64_t rows, hipStream_t st)
 {
-    if (a.c.width <= 64) attention_go<KIND, 64>(a, n, st);
-    else if (a.c.width <= 128) attention_go<KIND, 128>(a, n, st);
-    else attention_go<KIND, 256>(a, n, st);
+    const dim3 grid(grid_of((rows + 3) / 4)), block(echo::kBlock);
+    if (a.c.width <= 128) hipLaunchKernelGGL((echo::attention_join_kernel<128>), grid, block, 0, st, a, rows);
+    else hipLaunchKernelGGL((echo::attention_join_kernel<256>), grid, block, 0, st, a, rows);
+}
+
+template <int KIND>
+void attention_sized(echo::AttnArgs& a, const AttnPlan& n, bool page16, hipStream_t st)
+{
+    if (a.c.width <= 64) attention_go<KIND, 64>(a, n, page16, st);
+    else if (a.c.width <= 128) attention_go<KIND, 128>(a, n, page16, st);
+    else attention_go<KIND, 256>(a, n, page16, st);
 }
 
 }  // namespace
@@ -274,18 +303,18 @@ int echo_cache_attention(const echo_attention_args* p, void* workspace, size_t w
     a.q = p->q; a.out = p->out; a.lse = p->lse; a.ld_q = p->ld_q; a.ld_out = p->ld_out;
     a.window = (int)std::min(p->window, kMaxRows); a.group = (int)(p->q_heads / p->cache.heads); a.causal = p->causal;
     a.scale2 = (float)((double)p->scale * 1.4426950408889634);
-    a.splits = plan.splits;
-    a.part_o = (float*)workspace;
-    a.part_ml = (float*)((uint8_t*)workspace + plan.part_ml);
+    uint8_t* ws = (uint8_t*)workspace;
+    a.few_rows = plan.few && plan.tile ? (int)kFewBeside : 0;
+    a.few = {plan.few_splits, (float*)ws, (float*)(ws + plan.few_ml)};
+    a.tile = {plan.tile_splits, (float*)(ws + plan.tile_o), (float*)(ws + plan.tile_ml)};
     const hipStream_t st = (hipStream_t)stream;
     switch (p->cache.kind) {
-    case ECHO_BF16: attention_sized<echo::kCacheBf16>(a, plan, st); break;
-    case ECHO_I8: attention_sized<echo::kCacheI8>(a, plan, st); break;
-    default: attention_sized<echo::kCacheI4>(a, plan, st); break;
+    case ECHO_BF16: attention_sized<echo::kCacheBf16>(a, plan, paged16(p->cache), st); break;
+    case ECHO_I8: attention_sized<echo::kCacheI8>(a, plan, paged16(p->cache), st); break;
+    default: attention_sized<echo::kCacheI4>(a, plan, paged16(p->cache), st); break;
     }
-    if ((rc = check_launch()) || plan.splits == 1) return rc;
-    const int64_t rows = p->seqs.tokens * p->q_heads;
-    hipLaunchKernelGGL(echo::attention_join_kernel, dim3(grid_of((rows + 3) / 4)), dim3(echo::kBlock), 0, st, a, rows);
+    if ((rc = check_launch()) || !plan.total) return rc;
+    attention_join(a, p->seqs.tokens * p->q_heads, st);
     return check_launch();
 }
 

@@ -131,13 +131,14 @@ struct Int4Args {
 
 // codes 2i and 2i + 8 .. : the pairs (0, 4), (1, 5), (2, 6), (3, 7) of a word's
 // nibbles as bfloat16 16 + q
-__device__ __forceinline__ bf16x8 codes_bf16(uint32_t w)
+// (bias: two 16.0 in a register; an and-or takes only one literal)
+__device__ __forceinline__ bf16x8 codes_bf16(uint32_t w, uint32_t bias)
 {
     u32x4 r;
-    r.x = ((w << 3) & 0x00780078u) | 0x41804180u;
-    r.y = ((w >> 1) & 0x00780078u) | 0x41804180u;
-    r.z = ((w >> 5) & 0x00780078u) | 0x41804180u;
-    r.w = ((w >> 9) & 0x00780078u) | 0x41804180u;
+    r.x = ((w << 3) & 0x00780078u) | bias;
+    r.y = ((w >> 1) & 0x00780078u) | bias;
+    r.z = ((w >> 5) & 0x00780078u) | bias;
+    r.w = ((w >> 9) & 0x00780078u) | bias;
     return __builtin_bit_cast(bf16x8, r);
 }
 
@@ -216,6 +217,8 @@ __global__ __launch_bounds__(kInt4Threads) void linear_int4_kernel(const Int4Arg
     for (int t = 0; t < MT; ++t) xr[t] = min(m0 + 16 * t + col, a.M - 1) * a.ldx;
     const u32x4 one4 = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
     const bf16x8 ones = __builtin_bit_cast(bf16x8, one4);
+    uint32_t bias = 0x41804180u;
+    asm("" : "+v"(bias));
 
     f32x4 y[MT];
 #pragma unroll
@@ -234,7 +237,7 @@ __global__ __launch_bounds__(kInt4Threads) void linear_int4_kernel(const Int4Arg
             const u32x4 w = ld_codes4<4 * W>(wr, kl / 2, bytes);
 #pragma unroll
             for (int i = 0; i < W; ++i) {
-                const bf16x8 fw = codes_bf16(w[i]);
+                const bf16x8 fw = codes_bf16(w[i], bias);
 #pragma unroll
                 for (int t = 0; t < MT; ++t) {
                     bf16x8 fx[kPart];

@@ -647,8 +647,8 @@ int echo_cache_read(const echo_cache* cache, const echo_seqs* seqs, void* k, int
  *   q (device, in)     bfloat16 bits [tokens][q_heads * width], rows at ld_q
  *   out (device, out)  bfloat16 bits [tokens][q_heads * width], rows at ld_out
  *   lse (device, out)  fp32 [tokens][q_heads], or NULL
- * Constraints: q_heads a multiple of heads (ECHO_ESHAPE), tokens * q_heads <
- * 2^31 (ECHO_ESHAPE), scale finite, window >= 0, causal 0 or 1 (ECHO_EINVAL).
+ * Constraints: q_heads a multiple of heads, tokens * q_heads <= 2^29, seqs *
+ * heads <= 2^22 (ECHO_ESHAPE), scale finite, window >= 0, causal 0 or 1 (ECHO_EINVAL).
  * The workspace (device, 16-byte aligned, at least
  * echo_cache_attention_workspace_bytes of the same arguments) holds what the
  * parts of a long sequence leave to be joined; it may be NULL where that

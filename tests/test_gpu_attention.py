@@ -340,3 +340,12 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for (w, wl), (_, _, out, _), lse in zip(want, calls, lses):
         assert torch.equal(out.view(w.shape), w) and torch.equal(lse, wl)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("D,window,causal", [(64, 0, True), (128, 0, True), (128, 700, True), (64, 300, False), (96, 0, True)])
+def test_many_rows(kind, D, window, causal):
+    """Enough rows for the blocks of eight waves, beside a sequence of one row."""
+    new = [2500, 1, 1700]
+    assert sum(new) * 64 >= 256 * 1024
+    Case(kind, 2, 32, D, 64, new, [2500, 900, 2111], window=window, causal=causal).check()
