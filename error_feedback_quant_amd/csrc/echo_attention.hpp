@@ -678,13 +678,7 @@ void attention_tile_kernel(const AttnArgs a)
     const int64_t v = id % a.tiles;
     const int split = id / a.tiles;
     auto tile_base = [&](int b) { return (int64_t)a.s.starts[b] * a.group / kRows + b; };
-    int b = 0;
-    for (int top = a.s.seqs - 1; b < top;) {             // the last sequence whose tiles start at or below v
-        const int mid = (b + top + 1) >> 1;
-        if (__builtin_amdgcn_readfirstlane(tile_base(mid) <= v)) b = mid;
-        else top = mid - 1;
-    }
-    b = __builtin_amdgcn_readfirstlane(b);
+    const int b = last_at_most(a.s.seqs, v, tile_base);
     const RowSpan r = seq_span(a.s, b);
     const int rows = r.n * a.group;                      // below 2^31 with all heads
     if (a.few_rows && rows <= a.few_rows) return;        // the other kernel's
@@ -1002,8 +996,8 @@ __global__ __launch_bounds__(kBlock) void attention_join_kernel(const AttnArgs a
     for (int64_t at = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); at < rows; at += (int64_t)gridDim.x * 4) {
         const int64_t t = at / heads;
         const int qh = (int)(at - t * heads);
-        const int b = seq_of_row(a.s, t);
-        if (b < 0) continue;
+        const int b = last_at_most(a.s.seqs, t, [&](int i) { return (int64_t)a.s.starts[i]; });
+        if (!takes_row(a.s, b, t)) continue;
         const int64_t row0 = a.s.starts[b], n = (int64_t)a.s.starts[b + 1] - row0;
         const bool is_few = a.tile.splits == 0 || (a.few_rows && n * a.group <= a.few_rows);
         const AttnArgs::Parts& p = is_few ? a.few : a.tile;

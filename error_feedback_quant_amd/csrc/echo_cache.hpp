@@ -47,36 +47,46 @@ __device__ __forceinline__ int32_t cache_page(const SeqView& s, const CacheView&
     return (uint32_t)p < c.pages ? p : -1;
 }
 
-// Sequence of row t, -1 where it is none's (or its sequence's rows leave those
-// that there are): the last start at or below t.
-// The starts are on the device, so the host cannot give a map; a search of
-// log2(seqs) steps in L2 costs less than another launch.
-__device__ __forceinline__ int seq_of_row(const SeqView& s, int64_t t)
+// The last i of 0 .. n - 1 with f(i) <= v (f does not decrease; 0 where there
+// is none), for a v that the wave shares: 64 places at a time, so that it
+// costs one trip to the cache up to 64 sequences and two up to 4096.
+template <typename F>
+__device__ __forceinline__ int last_at_most(int n, int64_t v, F f)
 {
-    int lo = 0, hi = s.seqs;                    // the first start above t among 1 .. seqs is at lo + 1
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (s.starts[mid + 1] > t) hi = mid;
-        else lo = mid + 1;
+    const int lane = threadIdx.x & 63;
+    int lo = 0, hi = n;                         // it is in lo .. hi - 1
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 63) / 64;
+        const int64_t at = lo + (int64_t)(lane + 1) * step;
+        const int more = __popcll(__ballot(at < hi && f((int)at) <= v));
+        lo += more * step;
+        hi = min(lo + step, hi);
     }
-    const bool takes = lo < s.seqs && s.starts[lo] >= 0 && s.starts[lo] <= t && s.starts[lo + 1] <= s.tokens;
-    return takes ? lo : -1;
+    return __builtin_amdgcn_readfirstlane(lo);
 }
 
-struct CachePlace {
-    bool none;              // of no sequence
-    int32_t page;           // -1: no place
-    uint32_t slot;
-};
-
-__device__ __forceinline__ CachePlace place_of_row(const SeqView& s, const CacheView& c, int64_t t)
+// whether row t is sequence b's and b is a sequence that is taken
+__device__ __forceinline__ bool takes_row(const SeqView& s, int b, int64_t t)
 {
-    const int b = seq_of_row(s, t);
-    if (b < 0) return {true, -1, 0};
-    const int64_t pos = (int64_t)s.lens[b] - s.starts[b + 1] + t;
-    if (pos < 0 || pos >= s.capacity) return {false, -1, 0};
-    const uint32_t entry = (uint32_t)pos / c.page_tokens;          // capacity is below 2^32
-    return {false, cache_page(s, c, b, entry), (uint32_t)pos - entry * c.page_tokens};
+    return s.starts[b] >= 0 && s.starts[b] <= t && s.starts[b + 1] > t && s.starts[b + 1] <= s.tokens;
+}
+
+// Sequence of row t, -1 where it is none's (or its sequence's rows leave those
+// that there are).  from: the last one that starts at or below a row of the
+// wave that is not behind t.
+__device__ __forceinline__ int seq_of_row(const SeqView& s, int64_t t, int from)
+{
+    int lo = from;
+    for (int i = 0; i < 4 && lo + 1 < s.seqs && s.starts[lo + 1] <= t; ++i) ++lo;    // the next ones, as in a decode step
+    if (lo + 1 < s.seqs && s.starts[lo + 1] <= t) {
+        int hi = s.seqs - 1;
+        while (lo < hi) {
+            const int mid = lo + (hi - lo + 1) / 2;
+            if (s.starts[mid] <= t) lo = mid;
+            else hi = mid - 1;
+        }
+    }
+    return takes_row(s, lo, t) ? lo : -1;
 }
 
 struct CacheIoArgs {
@@ -87,94 +97,136 @@ struct CacheIoArgs {
     int64_t rows;           // tokens * heads, below 2^31
 };
 
-// L lanes share a row, 8 elements each; blockIdx.y 0 takes the keys, 1 the
-// values.  Both kernels are one pass over memory.
-template <int KIND, int L, bool BF16>
+// A wave's rows.  L lanes share a row, 8 elements each, so a pass takes 64 / L
+// rows and U passes follow each other with all their loads on their way.
+// Where a row lies takes two divisions, the sequence's numbers, its page and
+// 64-bit products, which would bound the kernels: each lane finds out about one
+// row and the others get its answer (60638 tokens x 8 x 128 from 8 bits: 92 us
+// with every lane for itself, 42 us so).
+template <int L, int U>
+struct IoRows {
+    static constexpr int kPass = 64 / L, kRows = kPass * U;
+    static_assert(kRows <= 64, "a lane to a row");
+    int64_t code, scale, x[2];      // of this lane's row; code -1: no place
+    bool none;                      // no row, or no sequence's
+    __device__ __forceinline__ IoRows(const CacheIoArgs& a)
+    {
+        const CacheView& c = a.c;
+        const int64_t wave = (int64_t)blockIdx.x * (kBlock / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        const int64_t first = wave * kRows, row = first + (threadIdx.x & 63u);
+        none = row >= a.rows || (threadIdx.x & 63u) >= (uint32_t)kRows;
+        code = -1;
+        scale = x[0] = x[1] = 0;
+        const uint32_t t0 = (uint32_t)min(first, a.rows - 1) / (uint32_t)c.heads;
+        const int from = last_at_most(a.s.seqs, t0, [&](int b) { return (int64_t)a.s.starts[b]; });
+        if (none) return;
+        const uint32_t t = (uint32_t)row / (uint32_t)c.heads, h = (uint32_t)row - t * (uint32_t)c.heads;
+        const int b = seq_of_row(a.s, t, from);
+        if (b < 0) {
+            none = true;
+            return;
+        }
+        x[0] = t * a.ld[0] + (int64_t)h * c.width;
+        x[1] = t * a.ld[1] + (int64_t)h * c.width;
+        const int64_t pos = (int64_t)a.s.lens[b] - a.s.starts[b + 1] + t;
+        if (pos < 0 || pos >= a.s.capacity) return;
+        const uint32_t entry = (uint32_t)pos / c.page_tokens, slot = (uint32_t)pos - entry * c.page_tokens;
+        const int32_t page = cache_page(a.s, c, b, entry);
+        if (page < 0) return;
+        code = page * c.ld_page + h * c.ld_head + slot * c.ld_token;
+        scale = page * c.ld_sp + h * c.ld_sh + slot;
+    }
+    // of the row that this lane has a share in, in pass u
+    struct Row {
+        int64_t code, scale, x;
+        bool none;
+    };
+    __device__ __forceinline__ Row of(int u, int part) const
+    {
+        const int from = u * kPass + (threadIdx.x & 63u) / L;
+        return {__shfl(code, from), __shfl(scale, from), __shfl(part ? x[1] : x[0], from), __shfl((int)none, from) != 0};
+    }
+};
+
+template <int KIND, int L, int U, bool BF16>
 __global__ __launch_bounds__(kBlock) void cache_write_kernel(const CacheIoArgs a)
 {
-    constexpr uint32_t kRows = kBlock / L;
     const CacheView& c = a.c;
     const int part = blockIdx.y, g = threadIdx.x % L, k = 8 * g;
     uint8_t* codes = part ? c.v : c.k;
     uint32_t* scales = part ? c.vs : c.ks;
-    for (int64_t r0 = (int64_t)blockIdx.x * kRows; r0 < a.rows; r0 += (int64_t)gridDim.x * kRows) {
-        const int64_t row = r0 + threadIdx.x / L;
-        const bool in = row < a.rows;
-        const uint32_t t = in ? (uint32_t)row / (uint32_t)c.heads : 0, h = in ? (uint32_t)row - t * (uint32_t)c.heads : 0;
-        const Raw8<BF16> raw = ld_raw8<BF16, false>(a.x[part], (int64_t)t * a.ld[part] + (int64_t)h * c.width, k,
-                                                    in ? c.width : 0);
-        CachePlace p = place_of_row(a.s, c, t);
-        const bool put = in && p.page >= 0;
-        const int64_t at = p.page * c.ld_page + (int64_t)h * c.ld_head + (int64_t)p.slot * c.ld_token + k;
-        const int64_t sat = p.page * c.ld_sp + (int64_t)h * c.ld_sh + p.slot;
-        float u[8];
+    const IoRows<L, U> rows(a);
+    typename IoRows<L, U>::Row r[U];
+    Raw8<BF16> raw[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        r[u] = rows.of(u, part);
+        raw[u] = ld_raw8<BF16, false>(a.x[part], r[u].x, k, r[u].none ? 0 : c.width);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const bool put = r[u].code >= 0, mine = put && k < c.width;
+        const int64_t at = r[u].code + k;
+        float v[8];
         uint32_t top = 0;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            u[e] = raw_get(raw, e);
-            top = max(top, abs_bits(u[e]));
+            v[e] = raw_get(raw[u], e);
+            top = max(top, abs_bits(v[e]));
         }
         if constexpr (KIND == kCacheBf16) {
-            if (put && k < c.width) {
-                float o[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) o[e] = u[e];
-                if constexpr (BF16) __builtin_memcpy(codes + 2 * at, raw.v, 16);
-                else st_row8<true, false>(codes, at, 0, 8, o);
+            if (mine) {
+                if constexpr (BF16) __builtin_memcpy(codes + 2 * at, raw[u].v, 16);
+                else st_row8<true, false>(codes, at, 0, 8, v);
             }
         } else if constexpr (KIND == kCacheI8) {
             const TokenScale s = token_scale(group_max_u32<L>(top));
             int q[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) q[e] = token_code(u[e], s.inv);
-            if (put && k < c.width) st_codes8<false>((int8_t*)codes, at, 0, 8, q);
-            if (put && g == 0) scales[sat] = __builtin_bit_cast(uint32_t, s.scale);
+            for (int e = 0; e < 8; ++e) q[e] = token_code(v[e], s.inv);
+            if (mine) st_codes8<false>((int8_t*)codes, at, 0, 8, q);
+            if (put && g == 0) scales[r[u].scale] = __builtin_bit_cast(uint32_t, s.scale);
         } else {
             uint32_t word;
-            const uint32_t q = quantize4<L>(u, top, word);
-            if (put && k < c.width) *(uint32_t*)(codes + at / 2) = q;
-            if (put && g == 0) scales[sat] = word;
+            const uint32_t q = quantize4<L>(v, top, word);
+            if (mine) *(uint32_t*)(codes + at / 2) = q;
+            if (put && g == 0) scales[r[u].scale] = word;
         }
     }
 }
 
-template <int KIND, int L, bool BF16>
+template <int KIND, int L, int U, bool BF16>
 __global__ __launch_bounds__(kBlock) void cache_read_kernel(const CacheIoArgs a)
 {
-    constexpr uint32_t kRows = kBlock / L;
     const CacheView& c = a.c;
     const int part = blockIdx.y, g = threadIdx.x % L, k = 8 * g;
     const uint8_t* codes = part ? c.v : c.k;
     const uint32_t* scales = part ? c.vs : c.ks;
-    for (int64_t r0 = (int64_t)blockIdx.x * kRows; r0 < a.rows; r0 += (int64_t)gridDim.x * kRows) {
-        const int64_t row = r0 + threadIdx.x / L;
-        if (row >= a.rows || k >= c.width) continue;
-        const uint32_t t = (uint32_t)row / (uint32_t)c.heads, h = (uint32_t)row - t * (uint32_t)c.heads;
-        const CachePlace p = place_of_row(a.s, c, t);
-        if (p.none) continue;
-        const int64_t to = (int64_t)t * a.ld[part] + (int64_t)h * c.width;
+    const IoRows<L, U> rows(a);
+    typename IoRows<L, U>::Row r[U];
+    constexpr int kWords = KIND == kCacheBf16 ? 4 : (KIND == kCacheI8 ? 2 : 1);
+    uint32_t w[U][kWords], word[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        r[u] = rows.of(u, part);
+        const bool get = r[u].code >= 0 && k < c.width;
+        word[u] = get && KIND != kCacheBf16 ? scales[r[u].scale] : 0u;
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) w[u][i] = 0;
+        if (get) __builtin_memcpy(w[u], __builtin_assume_aligned(codes + cache_bytes<KIND>(r[u].code + k), 4 * kWords), 4 * kWords);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        if (r[u].none || k >= c.width) continue;
         float v[8];
-        if (p.page < 0) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = __builtin_bit_cast(float, 0x7FC00000u);
-        } else {
-            const int64_t at = p.page * c.ld_page + (int64_t)h * c.ld_head + (int64_t)p.slot * c.ld_token + k;
-            const uint32_t word = KIND == kCacheBf16 ? 0u : scales[p.page * c.ld_sp + (int64_t)h * c.ld_sh + p.slot];
-            if constexpr (KIND == kCacheBf16) {
-                unpack_bf16x8(*(const u32x4*)(codes + 2 * at), v);
-            } else if constexpr (KIND == kCacheI8) {
-                const u32x2 w = *(const u32x2*)(codes + at);
-                const float s = __builtin_bit_cast(float, word);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = (float)(int8_t)((e < 4 ? w.x : w.y) >> (8 * (e & 3))) * s;
-            } else {
-                const uint32_t w = *(const uint32_t*)(codes + at / 2);
-                const float s = half_lo(word), z = half_hi(word);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = ((float)((w >> (4 * e)) & 15u) - z) * s;
-            }
+        for (int e = 0; e < 8; ++e) {
+            if constexpr (KIND == kCacheBf16) v[e] = e & 1 ? bf16_hi(w[u][e / 2]) : bf16_lo(w[u][e / 2]);
+            else if constexpr (KIND == kCacheI8) v[e] = (float)(int8_t)(w[u][e / 4] >> (8 * (e & 3))) * __builtin_bit_cast(float, word[u]);
+            else v[e] = ((float)((w[u][0] >> (4 * e)) & 15u) - half_hi(word[u])) * half_lo(word[u]);
+            if (r[u].code < 0) v[e] = __builtin_bit_cast(float, 0x7FC00000u);
         }
-        st_row8<BF16, false>(a.x[part], to, k, c.width, v);
+        st_row8<BF16, false>(a.x[part], r[u].x, k, c.width, v);
     }
 }
 

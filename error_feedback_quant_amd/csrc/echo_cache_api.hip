@@ -24,6 +24,7 @@ using echo::float_dtype;
 using echo::grid_of;
 using echo::kMaxRows;
 
+constexpr int64_t kMaxCacheRows = int64_t(1) << 26;       // of a call: 32 lanes each, keys and values, in 32 bits of threads
 constexpr int64_t kMaxStride = int64_t(1) << 40;        // of pages and heads, in elements
 constexpr int64_t kMaxLen = (int64_t(1) << 31) - (1 << 12);     // positions and the tiles behind them stay in 31 bits
 constexpr int64_t kCus = 256;
@@ -90,26 +91,32 @@ echo::SeqView seq_view(const echo_seqs& s, const echo_cache& c)
     return v;
 }
 
-template <int KIND, int L, bool WRITE>
+template <int KIND, int L, int U, bool WRITE>
 void cache_io_go(const echo::CacheIoArgs& a, bool bf16, hipStream_t st)
 {
-    const int64_t rows = echo::kBlock / L;
-    const dim3 grid(grid_of((a.rows + rows - 1) / rows), 2), block(echo::kBlock);
+    const int64_t rows = echo::kBlock / L * U;              // of a block
+    const dim3 grid((unsigned)((a.rows + rows - 1) / rows), 2), block(echo::kBlock);
     if constexpr (WRITE) {
-        if (bf16) hipLaunchKernelGGL((echo::cache_write_kernel<KIND, L, true>), grid, block, 0, st, a);
-        else hipLaunchKernelGGL((echo::cache_write_kernel<KIND, L, false>), grid, block, 0, st, a);
+        if (bf16) hipLaunchKernelGGL((echo::cache_write_kernel<KIND, L, U, true>), grid, block, 0, st, a);
+        else hipLaunchKernelGGL((echo::cache_write_kernel<KIND, L, U, false>), grid, block, 0, st, a);
     } else {
-        if (bf16) hipLaunchKernelGGL((echo::cache_read_kernel<KIND, L, true>), grid, block, 0, st, a);
-        else hipLaunchKernelGGL((echo::cache_read_kernel<KIND, L, false>), grid, block, 0, st, a);
+        if (bf16) hipLaunchKernelGGL((echo::cache_read_kernel<KIND, L, U, true>), grid, block, 0, st, a);
+        else hipLaunchKernelGGL((echo::cache_read_kernel<KIND, L, U, false>), grid, block, 0, st, a);
     }
 }
 
 template <int KIND, bool WRITE>
 void cache_io_sized(const echo::CacheIoArgs& a, bool bf16, hipStream_t st)
 {
-    if (a.c.width <= 64) cache_io_go<KIND, 8, WRITE>(a, bf16, st);
-    else if (a.c.width <= 128) cache_io_go<KIND, 16, WRITE>(a, bf16, st);
-    else cache_io_go<KIND, 32, WRITE>(a, bf16, st);
+    const int L = a.c.width <= 64 ? 8 : (a.c.width <= 128 ? 16 : 32);
+    const bool many = a.rows * L >= 16 * 256 * kCus;        // threads for all CUs many times over
+    auto go = [&](auto l) {
+        if (many) cache_io_go<KIND, decltype(l)::value, 4, WRITE>(a, bf16, st);
+        else cache_io_go<KIND, decltype(l)::value, 1, WRITE>(a, bf16, st);
+    };
+    if (L == 8) go(std::integral_constant<int, 8>{});
+    else if (L == 16) go(std::integral_constant<int, 16>{});
+    else go(std::integral_constant<int, 32>{});
 }
 
 template <bool WRITE>
@@ -120,7 +127,7 @@ int cache_io(const echo_cache* c, const echo_seqs* s, void* k, int64_t ld_k, voi
     int rc = check_cache(*c);
     if (rc) return rc;
     if ((rc = check_seqs(*s))) return rc;
-    if (s->tokens * c->heads > kMaxRows || bad_ld(ld_k, s->tokens, c->heads * c->width) ||
+    if (s->tokens * c->heads > kMaxCacheRows || bad_ld(ld_k, s->tokens, c->heads * c->width) ||
         bad_ld(ld_v, s->tokens, c->heads * c->width))
         return ECHO_ESHAPE;
     if (no_work(*s)) return ECHO_OK;

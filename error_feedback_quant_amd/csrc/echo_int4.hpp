@@ -109,11 +109,16 @@ __global__ __launch_bounds__(kBlock) void quantize_groups_kernel(const QuantGrou
 
 // ------------------------------------------------------------- few tokens --
 //
-// A block of 8 waves takes 16 channels and 16 MT tokens; its waves take every
-// eighth unit of K (128 elements, or a group of 256) and their sums meet in
-// LDS in a fixed order.  A lane's load of up to 16 bytes is its operand of the
-// next MFMAs: it holds 8 W consecutive codes of its row, W from 1 to 4, and
-// the fragments of x take the same order of k, which a sum does not see.
+// A block of 8 waves takes 16 NT channels and 16 MT tokens; its waves take
+// every eighth unit of K (128 elements, or a group of 256) and their sums meet
+// in LDS in a fixed order.  A lane's load of up to 16 bytes of codes is its
+// operand of the next MFMAs: it holds 8 W consecutive codes of its channel, W
+// from 1 to 4, and the fragments of x take the same order of k, which a sum
+// does not see.  x is the first operand, so a lane keeps one channel, whose
+// scales and zero points it needs, and four tokens of each tile.
+//
+// The weight passes once, without LDS, and a block's loads of DEPTH units are
+// on their way together, codes, parameters and tokens.
 
 constexpr int kInt4Waves = 8;
 constexpr int kInt4Threads = 64 * kInt4Waves;
@@ -196,86 +201,146 @@ __device__ __forceinline__ u32x4 ld_codes4(const uint8_t* row, int64_t at, int64
     return v;
 }
 
-template <int GROUP, int MT, bool BF16>
+template <int GROUP, int MT, int NT, int DEPTH, bool BF16>
 __global__ __launch_bounds__(kInt4Threads) void linear_int4_kernel(const Int4Args a)
 {
     constexpr int kPart = BF16 ? 1 : 3;
     constexpr int kSub = GROUP < 128 ? GROUP : 128;          // elements of K that one load of each lane covers
     constexpr int W = kSub / 32;                             // words of a lane's load
     constexpr int kUnit = GROUP < 128 ? 128 : GROUP;
-    __shared__ f32x4 part[kInt4Waves][MT][64];
+    constexpr int kLoads = kUnit / kSub, kGroups = kUnit / GROUP;       // of a unit
+    constexpr int kFrags = kUnit / 32;
+    __shared__ f32x4 part[kInt4Waves][MT * NT][64];
     const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const uint32_t col = lane & 15u, g = lane >> 4;
-    const int64_t n0 = (int64_t)blockIdx.x * 16, m0 = (int64_t)blockIdx.y * (16 * MT);
-    const uint8_t* wr = a.w + min(n0 + col, a.N - 1) * a.ldw;
+    const int64_t n0 = (int64_t)blockIdx.x * (16 * NT), m0 = (int64_t)blockIdx.y * (16 * MT);
     const int64_t bytes = ((int64_t)a.K + 1) / 2;
-    const uint32_t* pr[4];
+    // channels and tokens past the last one repeat it: their sums are not stored
+    const uint8_t* wr[NT];
+    const uint32_t* pr[NT];
 #pragma unroll
-    for (int v = 0; v < 4; ++v) pr[v] = a.p + min(n0 + 4 * g + v, a.N - 1) * a.ldp;
+    for (int j = 0; j < NT; ++j) {
+        const int64_t n = min(n0 + 16 * j + col, a.N - 1);
+        wr[j] = a.w + n * a.ldw;
+        pr[j] = a.p + n * a.ldp;
+    }
     int64_t xr[MT];
 #pragma unroll
     for (int t = 0; t < MT; ++t) xr[t] = min(m0 + 16 * t + col, a.M - 1) * a.ldx;
-    const u32x4 one4 = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+    uint32_t bias = 0x41804180u, one = 0x3F803F80u;          // two 16.0, two 1.0
+    asm("" : "+v"(bias), "+v"(one));
+    const u32x4 one4 = {one, one, one, one};
     const bf16x8 ones = __builtin_bit_cast(bf16x8, one4);
-    uint32_t bias = 0x41804180u;
-    asm("" : "+v"(bias));
 
-    f32x4 y[MT];
+    struct Unit {
+        u32x4 w[NT][kLoads];
+        uint32_t p[NT][kGroups];
+        Raw8<BF16> x[MT][kFrags];
+    };
+    auto k_of = [&](int u, int f) __attribute__((always_inline)) {     // first element of the lane's fragment f
+        return u * kUnit + f / W * kSub + 8 * (W * (int)g + f % W);
+    };
+    f32x4 y[MT][NT];
 #pragma unroll
-    for (int t = 0; t < MT; ++t) y[t] = f32x4{0, 0, 0, 0};
-    const int units = (int)(((int64_t)a.K + kUnit - 1) / kUnit);
-    for (int u = wave; u < units; u += kInt4Waves) {
-        f32x4 acc[MT], xs[MT];
+    for (int t = 0; t < MT; ++t)
 #pragma unroll
-        for (int s = 0; s < kUnit / kSub; ++s) {
-            const int k0 = u * kUnit + s * kSub;
-            if (s % (GROUP / kSub) == 0) {
+        for (int j = 0; j < NT; ++j) y[t][j] = f32x4{0, 0, 0, 0};
+    auto take = [&](const Unit& d) __attribute__((always_inline)) {
 #pragma unroll
-                for (int t = 0; t < MT; ++t) acc[t] = xs[t] = f32x4{0, 0, 0, 0};
+        for (int q = 0; q < kGroups; ++q) {
+            f32x4 acc[MT][NT], xs[MT];
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+                xs[t] = f32x4{0, 0, 0, 0};
+#pragma unroll
+                for (int j = 0; j < NT; ++j) acc[t][j] = f32x4{0, 0, 0, 0};
             }
-            const int kl = k0 + 8 * W * (int)g;              // of this lane
-            const u32x4 w = ld_codes4<4 * W>(wr, kl / 2, bytes);
 #pragma unroll
-            for (int i = 0; i < W; ++i) {
-                const bf16x8 fw = codes_bf16(w[i], bias);
+            for (int f = q * (kFrags / kGroups); f < (q + 1) * (kFrags / kGroups); ++f) {
+                bf16x8 fw[NT];
+#pragma unroll
+                for (int j = 0; j < NT; ++j) fw[j] = codes_bf16(d.w[j][f / W][f % W], bias);
 #pragma unroll
                 for (int t = 0; t < MT; ++t) {
                     bf16x8 fx[kPart];
-                    x_parts<BF16, kPart>(ld_raw8<BF16, true>(a.x, xr[t], kl + 8 * i, a.K), fx);
+                    x_parts<BF16, kPart>(d.x[t][f], fx);
 #pragma unroll
                     for (int p = 0; p < kPart; ++p) {
-                        acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fw, fx[p], acc[t], 0, 0, 0);
-                        xs[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, fx[p], xs[t], 0, 0, 0);
+                        xs[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fx[p], ones, xs[t], 0, 0, 0);
+#pragma unroll
+                        for (int j = 0; j < NT; ++j)
+                            acc[t][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fx[p], fw[j], acc[t][j], 0, 0, 0);
                     }
                 }
             }
-            if ((s + 1) % (GROUP / kSub) == 0 && k0 / GROUP * GROUP < a.K) {
-                const int grp = k0 / GROUP;
 #pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    const uint32_t word = pr[v][grp];
-                    const float sc = half_lo(word), z = half_hi(word) + 16.0f;
+            for (int j = 0; j < NT; ++j) {
+                const uint32_t word = d.p[j][q];
+                const float z = -16.0f - half_hi(word);
 #pragma unroll
-                    for (int t = 0; t < MT; ++t)
-                        y[t][v] = __builtin_fmaf(sc, __builtin_fmaf(-z, xs[t][v], acc[t][v]), y[t][v]);
-                }
+                for (int t = 0; t < MT; ++t)
+#pragma unroll
+                    for (int v = 0; v < 4; ++v)
+                        y[t][j][v] = __builtin_fmaf(half_lo(word), __builtin_fmaf(z, xs[t][v], acc[t][j][v]), y[t][j][v]);
             }
         }
+    };
+
+    const int full = a.K / kUnit;                            // units inside K
+    auto load = [&](Unit& d, int u) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+#pragma unroll
+            for (int s = 0; s < kLoads; ++s) __builtin_memcpy(&d.w[j][s], wr[j] + k_of(u, s * W) / 2, 4 * W);
+            __builtin_memcpy(d.p[j], pr[j] + (int64_t)u * kGroups, 4 * kGroups);
+        }
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+            for (int f = 0; f < kFrags; ++f)
+                __builtin_memcpy(d.x[t][f].v, (const char*)a.x + (xr[t] + k_of(u, f)) * (BF16 ? 2 : 4), sizeof(d.x[t][f].v));
+    };
+    for (int u0 = wave; u0 < full; u0 += kInt4Waves * DEPTH) {
+        Unit d[DEPTH];
+#pragma unroll
+        for (int i = 0; i < DEPTH; ++i) load(d[i], min(u0 + kInt4Waves * i, full - 1));       // without a condition they go out together
+#pragma unroll
+        for (int i = 0; i < DEPTH; ++i)
+            if (i == 0 || u0 + kInt4Waves * i < full) take(d[i]);
     }
-    // lane l of tile t holds channels 4 (l / 16) .. + 3 of token 16 t + l % 16
+    if (full * kUnit < a.K && (uint32_t)full % kInt4Waves == wave) {   // the unit that K ends in: x is 0 past K
+        Unit d;
 #pragma unroll
-    for (int t = 0; t < MT; ++t) part[wave][t][lane] = y[t];
+        for (int j = 0; j < NT; ++j) {
+#pragma unroll
+            for (int s = 0; s < kLoads; ++s) d.w[j][s] = ld_codes4<4 * W>(wr[j], k_of(full, s * W) / 2, bytes);
+#pragma unroll
+            for (int q = 0; q < kGroups; ++q) d.p[j][q] = full * kUnit + q * GROUP < a.K ? pr[j][(int64_t)full * kGroups + q] : 0u;
+        }
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+            for (int f = 0; f < kFrags; ++f) d.x[t][f] = ld_raw8<BF16, true>(a.x, xr[t], k_of(full, f), a.K);
+        take(d);
+    }
+    // lane l holds channel l % 16 and tokens 4 (l / 16) .. + 3 of each tile
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) part[wave][t * NT + j][lane] = y[t][j];
     __syncthreads();
-    for (uint32_t i = tid; i < 64 * MT; i += kInt4Threads) {
-        f32x4 s = part[0][i >> 6][i & 63u];
+    for (uint32_t i = tid; i < 64 * MT * NT; i += kInt4Threads) {
+        const uint32_t tile = i >> 6, l = i & 63u;
+        f32x4 s = part[0][tile][l];
 #pragma unroll
-        for (int w = 1; w < kInt4Waves; ++w) s += part[w][i >> 6][i & 63u];
-        const int64_t m = m0 + 16 * (i >> 6) + (i & 15u);
-        const int64_t n = n0 + 4 * ((i & 63u) >> 4);
-        if (m >= a.M) continue;
+        for (int w = 1; w < kInt4Waves; ++w) s += part[w][tile][l];
+        const int64_t m = m0 + 16 * (tile / NT) + 4 * (l >> 4);
+        const int64_t n = n0 + 16 * (tile % NT) + (l & 15u);
+        if (n >= a.N) continue;
+        const float b = a.bias ? a.bias[n] : 0.0f;
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            if (n + e < a.N) st_elem(a.y, a.bf16, m * a.ldy + n + e, a.bias ? s[e] + a.bias[n + e] : s[e]);
+            if (m + e < a.M) st_elem(a.y, a.bf16, (m + e) * a.ldy + n, a.bias ? s[e] + b : s[e]);
     }
 }
 

@@ -37,22 +37,37 @@ void quantize_go(const echo::QuantGroupArgs& a, bool bf16, hipStream_t st)
     else hipLaunchKernelGGL((echo::quantize_groups_kernel<L, false>), grid, block, 0, st, a);
 }
 
-constexpr int64_t kMostTiles = int64_t(1) << 23;        // of 16 channels by 64 tokens: a launch's threads stay in 32 bits
+constexpr int64_t kMostTiles = (int64_t(1) << 23) - 1;  // of 16 channels by 32 tokens: a launch's threads stay in 32 bits
 
-template <int GROUP, int MT>
-void linear_go(const echo::Int4Args& a, bool x_bf16, hipStream_t st)
+template <int GROUP, int MT, int NT, int DEPTH, bool BF16>
+void linear_go(const echo::Int4Args& a, hipStream_t st)
 {
-    const dim3 grid((unsigned)((a.N + 15) / 16), (unsigned)((a.M + 16 * MT - 1) / (16 * MT))), block(echo::kInt4Threads);
-    if (x_bf16) hipLaunchKernelGGL((echo::linear_int4_kernel<GROUP, MT, true>), grid, block, 0, st, a);
-    else hipLaunchKernelGGL((echo::linear_int4_kernel<GROUP, MT, false>), grid, block, 0, st, a);
+    const dim3 grid((unsigned)((a.N + 16 * NT - 1) / (16 * NT)), (unsigned)((a.M + 16 * MT - 1) / (16 * MT)));
+    hipLaunchKernelGGL((echo::linear_int4_kernel<GROUP, MT, NT, DEPTH, BF16>), grid, dim3(echo::kInt4Threads), 0, st, a);
 }
+#ifndef N4
+#define N4 2
+#endif
+#ifndef D1
+#define D1 4
+#endif
+#ifndef D2
+#define D2 2
+#endif
 
+// fp32 tokens are three operands each, so a block takes half as many
 template <int GROUP>
 void linear_sized(const echo::Int4Args& a, bool x_bf16, hipStream_t st)
 {
-    if (a.M <= 16) linear_go<GROUP, 1>(a, x_bf16, st);
-    else if (a.M <= 32) linear_go<GROUP, 2>(a, x_bf16, st);
-    else linear_go<GROUP, 4>(a, x_bf16, st);
+    constexpr int kUnits = GROUP == 256 ? 1 : 2;             // of 256 elements
+    if (x_bf16) {
+        if (a.M <= 16) linear_go<GROUP, 1, 1, kUnits * D1 / 2, true>(a, st);
+        else if (a.M <= 32) linear_go<GROUP, 2, 1, kUnits * D2 / 2, true>(a, st);
+        else linear_go<GROUP, 4, N4, 1, true>(a, st);
+    } else {
+        if (a.M <= 16) linear_go<GROUP, 1, 1, kUnits, false>(a, st);
+        else linear_go<GROUP, 2, 1, 1, false>(a, st);
+    }
 }
 
 }  // namespace
@@ -95,7 +110,7 @@ int echo_linear_int4(const void* x, int64_t ldx, int x_dtype, const uint8_t* w, 
     if (bad_dim(M, kMaxRows) || bad_dim(N, kMaxRows) || bad_dim(K, kMaxK)) return ECHO_ESHAPE;
     if (bad_ld(ldx, M, K) || bad_ld(ldw, N, (K + 1) / 2) || bad_ld(ldp, N, groups_of(K, group)) || bad_ld(ldy, M, N))
         return ECHO_ESHAPE;
-    if ((M + 63) / 64 * ((N + 15) / 16) > kMostTiles || M > 64 * 65535) return ECHO_ESHAPE;
+    if ((M + 31) / 32 * ((N + 15) / 16) > kMostTiles || M > 32 * 65535) return ECHO_ESHAPE;
     if (M == 0 || N == 0) return ECHO_OK;
     if ((K && (!x || !w || !params)) || !y) return ECHO_EINVAL;
     if (!aligned_elem(x, x_dtype) || !aligned_to(params, 4) || !aligned_to(bias, 4) || !aligned_elem(y, y_dtype))

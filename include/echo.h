@@ -532,15 +532,15 @@ int echo_quantize_groups(const void* x, int64_t ldx, int x_dtype, int64_t T, int
  * sums is fixed: equal calls give equal bits.  z is an integer from 0 to 15
  * (what the quantizer above makes); other zero points round in z + 16.
  * A token that holds an infinity or a NaN is NaN throughout.  It is made for
- * few tokens: every 64 tokens read the weight again.
+ * few tokens: every 64 tokens (32 in fp32) read the weight again.
  *
  *   x (device, in)      [M][K], ECHO_F32 or ECHO_BF16, rows at ldx
  *   w (device, in)      [N][(K + 1) / 2] bytes of codes, rows at ldw bytes
  *   params (device, in) [N][ceil(K / group)], rows at ldp
  *   bias (device, in)   fp32 [N] or NULL
  *   y (device, out)     [M][N], ECHO_F32 or ECHO_BF16, rows at ldy
- * Constraints: group as above; 0 <= K <= 2^30, M and N < 2^31 and at most
- * 2^23 tiles of 16 channels by 64 tokens (ECHO_ESHAPE).  M or N of 0 enqueues
+ * Constraints: group as above; 0 <= K <= 2^30, M <= 2^21 - 32, N < 2^31 and
+ * fewer than 2^23 tiles of 16 channels by 32 tokens (ECHO_ESHAPE).  M or N of 0 enqueues
  * nothing; K of 0 gives y = bias (or 0).  The workspace (device, 16-byte
  * aligned, at least echo_linear_int4_workspace_bytes) may be NULL where that
  * function returns 0.
@@ -613,7 +613,7 @@ typedef struct echo_seqs {
  * same.  Slots of other tokens are not touched.
  *   k, v (device, in)  [tokens][heads * width], ECHO_F32 or ECHO_BF16 (rounded
  *                      once into an ECHO_BF16 cache), rows at ld_k and ld_v
- * Constraints: tokens * heads < 2^31 (ECHO_ESHAPE).
+ * Constraints: tokens * heads <= 2^26 (ECHO_ESHAPE).
  */
 int echo_cache_write(const echo_cache* cache, const echo_seqs* seqs, const void* k, int64_t ld_k, const void* v,
                      int64_t ld_v, int dtype, void* stream);
@@ -623,6 +623,7 @@ int echo_cache_write(const echo_cache* cache, const echo_seqs* seqs, const void*
  * in fp32, rounded once to bf16 where k and v are bf16.  Tokens without a
  * place give NaN.  With starts the sums of lens it reads whole sequences.
  *   k, v (device, out)  [tokens][heads * width], ECHO_F32 or ECHO_BF16
+ * Constraints: as for echo_cache_write.
  */
 int echo_cache_read(const echo_cache* cache, const echo_seqs* seqs, void* k, int64_t ld_k, void* v, int64_t ld_v,
                     int dtype, void* stream);
