@@ -615,8 +615,8 @@ void attention_few_kernel(const AttnArgs a)
 
 // ------------------------------------------------------------- many rows --
 //
-// A block of four waves takes 128 QR rows of one sequence and head of the
-// cache, 32 QR to a wave, and walks over the tokens in tiles of 8192 / DP.  A
+// A block of W waves takes 32 W rows of one sequence and head of the cache,
+// 32 to a wave, and walks over the tokens in tiles of 2048 W / DP.  A
 // tile is loaded into registers while the one before it is multiplied, turned
 // into bfloat16 and laid into one of two stages of LDS, in the order of the
 // matrix operands: every read of a fragment is 64 consecutive 16-byte words.
@@ -652,12 +652,12 @@ __device__ __forceinline__ float unit_get(const RawUnit<KIND>& r, int e, float z
     else return (float)((r.w[0] >> (4 * e)) & 15u) - z;
 }
 
-template <int KIND, int DP, int W, int QR, bool PAGE16>
+template <int KIND, int DP, int W, bool PAGE16>
 __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(DP == 256 ? 1 : 2, DP == 256 ? 1 : 2)))
 void attention_tile_kernel(const AttnArgs a)
 {
     using S = TileShape<DP, W>;
-    constexpr int kRows = 32 * QR * W;
+    constexpr int kRows = 32 * W;
     constexpr int kWords = S::kTokens * DP / 8;          // of 16 bytes, in a stage of k or v
     __shared__ __align__(16) u32x4 sk[2][kWords], sv[2][kWords];
     __shared__ __align__(16) float sks[2][S::kTokens], svs[2][S::kTokens];      // k's scale times scale2, v's scale
@@ -695,32 +695,30 @@ void attention_tile_kernel(const AttnArgs a)
     const uint32_t* scales = (is_v ? c.vs : c.ks) + h * c.ld_sh;
     const bool unit_in = 8 * su < c.width;
     const int64_t token_bytes = cache_bytes<KIND>(c.ld_token);
+    // where k's unit of the octet's first token goes, in bytes; token e then lies at an exclusive or with 16 e
+    const uint32_t k_at = 16u * (((token0 >> 5) * S::kUnits + su) * 32 + (token0 & 31) + (su & 7));
 
     const int64_t rt = ((int64_t)rows + kRows - 1) / kRows - 1 - (v - ((int64_t)r.row0 * a.group / kRows + b));
     if (rt < 0 || rt * kRows >= rows) return;
     {
-        // this lane's rows
-        int hi[QR], lo[QR];
-        bf16x8 fq[QR][DP / 16];
+        // this lane's row
+        const int64_t rr = rt * kRows + wave * 32 + col;
+        const bool there = rr < rows;
+        const int i = there ? (int)rr / a.group : 0;
+        const int64_t t = r.row0 + i;
+        const int qh = h * a.group + (there ? (int)rr - i * a.group : 0);
+        const int pos = r.pos(i);
+        const int hi = there ? (a.causal ? pos : r.len - 1) : -1;            // it sees lo .. hi
+        const int lo = a.window ? pos - a.window + 1 : 0;
+        bf16x8 fq[DP / 16];
 #pragma unroll
-        for (int x = 0; x < QR; ++x) {
-            const int64_t rr = rt * kRows + (wave * QR + x) * 32 + col;
-            const bool there = rr < rows;
-            const int i = there ? (int)rr / a.group : 0;
-            const int qh = h * a.group + (there ? (int)rr - i * a.group : 0);
-            const int pos = r.pos(i);
-            hi[x] = there ? (a.causal ? pos : r.len - 1) : -1;           // it sees lo .. hi
-            lo[x] = a.window ? pos - a.window + 1 : 0;
-#pragma unroll
-            for (int ks = 0; ks < DP / 16; ++ks)
-                fq[x][ks] = __builtin_bit_cast(
-                    bf16x8, ld_raw8<true, false>(a.q, (int64_t)(r.row0 + i) * a.ld_q + (int64_t)qh * c.width, 16 * ks + 8 * half,
-                                                 c.width).v[0]);
-        }
+        for (int ks = 0; ks < DP / 16; ++ks)
+            fq[ks] = __builtin_bit_cast(
+                bf16x8, ld_raw8<true, false>(a.q, t * a.ld_q + (int64_t)qh * c.width, 16 * ks + 8 * half, c.width).v[0]);
         int some_hi = -1, some_lo = INT32_MAX;               // no row sees further than this
-        const int64_t first_row = rt * kRows + wave * QR * 32;
+        const int64_t first_row = rt * kRows + wave * 32;
         if (first_row < rows) {
-            some_hi = a.causal ? r.pos(((int)min(first_row + 32 * QR, (int64_t)rows) - 1) / a.group) : r.len - 1;
+            some_hi = a.causal ? r.pos(((int)min(first_row + 32, (int64_t)rows) - 1) / a.group) : r.len - 1;
             some_lo = a.window ? r.pos((int)first_row / a.group) - a.window + 1 : 0;
         }
         int begin, end;
@@ -791,7 +789,6 @@ void attention_tile_kernel(const AttnArgs a)
             if (!is_v) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const int t = token0 + e;
                     u32x4 o;
                     if constexpr (KIND == kCacheBf16) {
                         o = u32x4{raw[e].w[0], raw[e].w[1], raw[e].w[2], raw[e].w[3]};
@@ -801,7 +798,7 @@ void attention_tile_kernel(const AttnArgs a)
                         for (int i = 0; i < 4; ++i)
                             o[i] = upper_pair(unit_get<KIND>(raw[e], 2 * i, z[e]), unit_get<KIND>(raw[e], 2 * i + 1, z[e]));
                     }
-                    sk[buf][((t >> 5) * S::kUnits + su) * 32 + ((t & 31) ^ (su & 7))] = o;
+                    *(u32x4*)((uint8_t*)sk[buf] + (k_at ^ (16u * e))) = o;
                 }
                 return;
             }
@@ -835,95 +832,122 @@ void attention_tile_kernel(const AttnArgs a)
             }
         };
 
-        f32x16 o[QR][S::kParts];
-        RowSum sum[QR];
+        f32x16 o[S::kParts];
 #pragma unroll
-        for (int x = 0; x < QR; ++x)
+        for (int p = 0; p < S::kParts; ++p)
 #pragma unroll
-            for (int p = 0; p < S::kParts; ++p)
+            for (int v = 0; v < 16; ++v) o[p][v] = 0.0f;
+        RowSum sum;
+        // scores of 32 tokens before they are scaled
+        auto first = [&](int buf, int sub) __attribute__((always_inline)) {
+            f32x16 acc;
 #pragma unroll
-                for (int v = 0; v < 16; ++v) o[x][p][v] = 0.0f;
-        auto first = [&](int buf, int sub, f32x16 (&acc)[QR]) __attribute__((always_inline)) {
-#pragma unroll
-            for (int x = 0; x < QR; ++x)
-#pragma unroll
-                for (int v = 0; v < 16; ++v) acc[x][v] = 0.0f;
+            for (int v = 0; v < 16; ++v) acc[v] = 0.0f;
 #pragma unroll
             for (int ks = 0; ks < DP / 16; ++ks) {
                 const int u = 2 * ks + half;
                 const bf16x8 fk = __builtin_bit_cast(bf16x8, sk[buf][(sub * S::kUnits + u) * 32 + (col ^ (u & 7))]);
-#pragma unroll
-                for (int x = 0; x < QR; ++x) acc[x] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fk, fq[x][ks], acc[x], 0, 0, 0);
+                acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fk, fq[ks], acc, 0, 0, 0);
             }
+            return acc;
         };
-        auto second = [&](auto masked, int buf, int sub, int p0, f32x16 (&acc)[QR]) __attribute__((always_inline)) {
-            constexpr bool MASKED = decltype(masked)::value;
-            bf16x8 fp[QR][2];
+        // z of them, with the mask, and the largest
+        auto scores = [&](auto masked, int buf, int sub, int p0, const f32x16& acc, float (&z)[16], uint32_t& seen)
+            __attribute__((always_inline)) {
 #pragma unroll
-            for (int x = 0; x < QR; ++x) {
-                float z[16];
-                uint32_t seen = 0xFFFFu, odd = 0;            // tokens that the row sees; whose v holds no number
+            for (int j = 0; j < 4; ++j) {
+                f32x4 ks = f32x4{a.scale2, a.scale2, a.scale2, a.scale2};
+                if constexpr (KIND != kCacheBf16) ks = *(const f32x4*)&sks[buf][32 * sub + 8 * j + 4 * half];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    f32x4 ks = f32x4{a.scale2, a.scale2, a.scale2, a.scale2};
-                    if constexpr (KIND != kCacheBf16) ks = *(const f32x4*)&sks[buf][32 * sub + 8 * j + 4 * half];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) z[4 * j + k] = __builtin_fmaf(acc[x][4 * j + k], ks[k], sum[x].minus_m);
-                }
-                if constexpr (MASKED) {
-                    if constexpr (KIND == kCacheBf16) odd = sodd[buf][4 * sub + half] | (uint32_t)sodd[buf][4 * sub + 2 + half] << 8;
-#pragma unroll
-                    for (int v = 0; v < 16; ++v) {
-                        const int p = p0 + 32 * sub + 8 * (v >> 2) + 4 * half + (v & 3);
-                        if (!(p >= lo[x] && p <= hi[x] && p < end)) {
-                            z[v] = neg_inf();
-                            seen &= ~(1u << v);
-                        }
-                    }
-                }
-                float top = z[0];
-#pragma unroll
-                for (int v = 1; v < 16; ++v) top = fmaxf(top, z[v]);
-                row_raise<2>(sum[x], z, top, [&](float by) {
-#pragma unroll
-                    for (int p = 0; p < S::kParts; ++p) o[x][p] *= by;
-                });
-                float p[16];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    f32x4 vs;
-                    if constexpr (KIND != kCacheBf16) vs = *(const f32x4*)&svs[buf][32 * sub + 8 * j + 4 * half];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int v = 4 * j + k;
-                        p[v] = exp2_fast(z[v]);
-                        sum[x].l += p[v];
-                        if constexpr (KIND != kCacheBf16) p[v] *= vs[k];
-                        if constexpr (MASKED) {
-                            if (KIND == kCacheBf16 && ((odd >> v) & 1u)) p[v] = nan_f32();
-                            if (!((seen >> v) & 1u)) p[v] = 0.0f;
-                        }
-                    }
-                }
-                fp[x][0] = to_bf16x8(p);
-                fp[x][1] = to_bf16x8(p + 8);
+                for (int k = 0; k < 4; ++k) z[4 * j + k] = __builtin_fmaf(acc[4 * j + k], ks[k], sum.minus_m);
             }
+            if constexpr (decltype(masked)::value) {
+                seen = 0;
+#pragma unroll
+                for (int v = 0; v < 16; ++v) {
+                    const int p = p0 + 32 * sub + 8 * (v >> 2) + 4 * half + (v & 3);
+                    const bool sees = (p >= lo) & (p <= hi) & (p < end);
+                    z[v] = sees ? z[v] : neg_inf();
+                    seen |= sees ? 1u << v : 0u;
+                }
+            }
+            float top = z[0];
+#pragma unroll
+            for (int v = 1; v < 16; ++v) top = fmaxf(top, z[v]);
+            return top;
+        };
+        // the weights as the second product's operands
+        auto weights = [&](auto masked, int buf, int sub, const float (&z)[16], uint32_t seen, bf16x8 (&fp)[2])
+            __attribute__((always_inline)) {
+            uint32_t odd = 0;                                // tokens whose v holds no number
+            if constexpr (decltype(masked)::value && KIND == kCacheBf16)
+                odd = sodd[buf][4 * sub + half] | (uint32_t)sodd[buf][4 * sub + 2 + half] << 8;
+            float p[16];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                f32x4 vs;
+                if constexpr (KIND != kCacheBf16) vs = *(const f32x4*)&svs[buf][32 * sub + 8 * j + 4 * half];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int v = 4 * j + k;
+                    p[v] = exp2_fast(z[v]);
+                    sum.l += p[v];
+                    if constexpr (KIND != kCacheBf16) p[v] *= vs[k];
+                    if constexpr (decltype(masked)::value) {
+                        if (KIND == kCacheBf16 && ((odd >> v) & 1u)) p[v] = nan_f32();
+                        if (!((seen >> v) & 1u)) p[v] = 0.0f;
+                    }
+                }
+            }
+            fp[0] = to_bf16x8(p);
+            fp[1] = to_bf16x8(p + 8);
+        };
+        auto second = [&](int buf, int sub, const bf16x8 (&fp)[2]) __attribute__((always_inline)) {
 #pragma unroll
             for (int st = 0; st < 2; ++st)
 #pragma unroll
                 for (int p = 0; p < S::kParts; ++p) {
                     const bf16x8 fv = __builtin_bit_cast(bf16x8, sv[buf][(((2 * sub + st) * S::kParts + p) * 2 + half) * 32 + col]);
-#pragma unroll
-                    for (int x = 0; x < QR; ++x) o[x][p] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fv, fp[x][st], o[x][p], 0, 0, 0);
+                    o[p] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fv, fp[st], o[p], 0, 0, 0);
                 }
         };
+        // The matrix cores work while the weights of one 32 tokens are made,
+        // on the scores of the next, and then on the weights while those
+        // scores are scaled and compared; the order is asked for, since
+        // matrix instructions in a row would hold up the wave's others.
         auto products = [&](auto masked, int buf, int p0) __attribute__((always_inline)) {
-            f32x16 acc[2][QR];
-            first(buf, 0, acc[0]);
+            float z[16];
+            uint32_t seen = 0xFFFFu;
+            f32x16 acc = first(buf, 0);
+            float top = scores(masked, buf, 0, p0, acc, z, seen);
 #pragma unroll
             for (int sub = 0; sub < S::kSubs; ++sub) {
-                if (sub + 1 < S::kSubs) first(buf, sub + 1, acc[(sub + 1) & 1]);
-                second(masked, buf, sub, p0, acc[sub & 1]);
+                row_raise<2>(sum, z, top, [&](float by) __attribute__((always_inline)) {
+#pragma unroll
+                    for (int p = 0; p < S::kParts; ++p) o[p] *= by;
+                });
+                bf16x8 fp[2];
+                if (sub + 1 < S::kSubs) acc = first(buf, sub + 1);
+                weights(masked, buf, sub, z, seen, fp);
+                second(buf, sub, fp);
+                if (sub + 1 < S::kSubs) {
+                    top = scores(masked, buf, sub + 1, p0, acc, z, seen);
+                    if constexpr (!decltype(masked)::value) {
+                        __builtin_amdgcn_sched_group_barrier(0x100, 10, 0);                // reads of LDS go ahead
+#pragma unroll
+                        for (int i = 0; i < DP / 16; ++i) {
+                            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);             // a matrix product
+                            __builtin_amdgcn_sched_group_barrier(0x402, 56 * 16 / DP, 0);  // what the vector unit does meanwhile
+                            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 2 * S::kParts; ++i) {
+                            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                            __builtin_amdgcn_sched_group_barrier(0x402, 12 / S::kParts, 0);
+                            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+                        }
+                    }
+                }
             }
         };
 
@@ -948,16 +972,13 @@ void attention_tile_kernel(const AttnArgs a)
             while (p0 < end && whole(p0)) turn(std::false_type{});
         }
 
-        // a lane holds, of its rows, units of 8 elements
-#pragma unroll
-        for (int x = 0; x < QR; ++x) {
-            float l = sum[x].l + __shfl_xor(sum[x].l, 32);
-            const int64_t rr = rt * kRows + (wave * QR + x) * 32 + col;
-            if (rr >= rows) continue;
-            const int64_t i = (int)rr / a.group, t = r.row0 + i;
-            const int64_t qh = h * a.group + (rr - i * a.group), at = t * c.heads * a.group + qh;
-            if (hi[x] >= a.s.capacity) l = nan_f32();     // it sees tokens that the table does not hold
-            const float inv = a.tile.splits > 1 ? 1.0f : (l == 0.0f ? 0.0f : 1.0f / l);
+        // a lane holds, of its row, units of 8 elements
+        float l = sum.l + __shfl_xor(sum.l, 32);
+        if (there) {
+            const int64_t at = t * c.heads * a.group + qh;
+            if (hi >= a.s.capacity) l = nan_f32();           // it sees tokens that the table does not hold
+            const bool parts = a.tile.splits > 1;
+            const float inv = parts ? 1.0f : (l == 0.0f ? 0.0f : 1.0f / l);
             constexpr int kSlots = 16 / S::kEach;
 #pragma unroll
             for (int k = 0; k < kSlots; ++k) {
@@ -965,18 +986,18 @@ void attention_tile_kernel(const AttnArgs a)
                 if (d >= c.width) continue;
                 float e[8];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) e[j] = o[x][j / S::kEach][k + kSlots * (j % S::kEach)] * inv;
-                if (a.tile.splits > 1) {
+                for (int j = 0; j < 8; ++j) e[j] = o[j / S::kEach][k + kSlots * (j % S::kEach)] * inv;
+                if (parts) {
                     float* po = a.tile.o + (at * a.tile.splits + split) * c.width + d;
                     *(f32x4*)po = f32x4{e[0], e[1], e[2], e[3]};
                     *(f32x4*)(po + 4) = f32x4{e[4], e[5], e[6], e[7]};
                 } else {
-                    st_row8<true, false>(a.out, t * a.ld_out + qh * c.width, d, c.width, e);
+                    st_row8<true, false>(a.out, t * a.ld_out + (int64_t)qh * c.width, d, c.width, e);
                 }
             }
             if (half == 0) {
-                if (a.tile.splits > 1) *(f32x2*)(a.tile.ml + 2 * (at * a.tile.splits + split)) = f32x2{sum[x].m(), l};
-                else if (a.lse) a.lse[at] = row_lse(sum[x].m(), l);
+                if (parts) *(f32x2*)(a.tile.ml + 2 * (at * a.tile.splits + split)) = f32x2{sum.m(), l};
+                else if (a.lse) a.lse[at] = row_lse(sum.m(), l);
             }
         }
     }

@@ -241,11 +241,11 @@ void attention_go(echo::AttnArgs& a, const AttnPlan& n, bool page16, hipStream_t
         a.tiles = (uint32_t)n.tile_tiles;
         const dim3 grid((unsigned)(n.tile_tiles * a.c.heads * n.tile_splits)), block(64 * n.tile_waves);
         if (!page16) {
-            hipLaunchKernelGGL((echo::attention_tile_kernel<KIND, DP, 4, 1, false>), grid, block, 0, st, a);
+            hipLaunchKernelGGL((echo::attention_tile_kernel<KIND, DP, 4, false>), grid, block, 0, st, a);
         } else if (n.tile_waves == 4) {
-            hipLaunchKernelGGL((echo::attention_tile_kernel<KIND, DP, 4, 1, true>), grid, block, 0, st, a);
+            hipLaunchKernelGGL((echo::attention_tile_kernel<KIND, DP, 4, true>), grid, block, 0, st, a);
         } else if constexpr (DP < 256) {
-            hipLaunchKernelGGL((echo::attention_tile_kernel<KIND, DP, 8, 1, true>), grid, block, 0, st, a);
+            hipLaunchKernelGGL((echo::attention_tile_kernel<KIND, DP, 8, true>), grid, block, 0, st, a);
         }
     }
     if (n.few) {
