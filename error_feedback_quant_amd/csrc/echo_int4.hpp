@@ -111,13 +111,15 @@ __global__ __launch_bounds__(kBlock) void quantize_groups_kernel(const QuantGrou
 //
 // A block of 8 waves takes 16 NT channels and 16 MT tokens; its waves take
 // every eighth unit of K (128 elements, or a group of 256) and their sums meet
-// in LDS in a fixed order.  A lane's load of up to 16 bytes of codes is its
-// operand of the next MFMAs: it holds 8 W consecutive codes of its channel, W
-// from 1 to 4, and the fragments of x take the same order of k, which a sum
-// does not see.  x is the first operand, so a lane keeps one channel, whose
-// scales and zero points it needs, and four tokens of each tile.
+// in LDS in a fixed order.  x is the first operand, so a lane keeps one
+// channel, whose scales and zero points it needs, and four tokens of a tile.
 //
-// The weight passes once, without LDS, and a block's loads of DEPTH units are
+// The weight passes once, without LDS: a lane loads 16 bytes, 32 codes of its
+// channel, and the four lanes of a channel exchange words so that each has the
+// codes that stand beside its 8 elements of x in an MFMA.  So both loads are
+// whole: 64 contiguous bytes of a row for four lanes (with
+// the codes as loaded and x in their order, 16-byte pieces at distances of 64,
+// 27 x 1001 x 3583 took 11.4 us, so 10.0).  A block's loads of DEPTH units are
 // on their way together, codes, parameters and tokens.
 
 constexpr int kInt4Waves = 8;
@@ -187,28 +189,34 @@ __device__ __forceinline__ void x_parts(const Raw8<BF16>& r, bf16x8 (&f)[P])
     }
 }
 
-// BYTES (4, 8 or 16) of codes from byte `at` of a row of `bytes`, zeros past
-// its end
-template <int BYTES>
-__device__ __forceinline__ u32x4 ld_codes4(const uint8_t* row, int64_t at, int64_t bytes)
+// 16 bytes of codes from byte `at` of a row of `bytes`, zeros past its end
+__device__ __forceinline__ u32x4 ld_codes16(const uint8_t* row, int64_t at, int64_t bytes)
 {
     u32x4 v = {0, 0, 0, 0};
-    if (at + BYTES <= bytes) {
-        __builtin_memcpy(&v, row + at, BYTES);
+    if (at + 16 <= bytes) {
+        __builtin_memcpy(&v, row + at, 16);
     } else {
-        for (int i = 0; i < BYTES && at + i < bytes; ++i) v[i / 4] |= (uint32_t)row[at + i] << (8 * (i & 3));
+        for (int i = 0; i < 16 && at + i < bytes; ++i) v[i / 4] |= (uint32_t)row[at + i] << (8 * (i & 3));
     }
     return v;
+}
+
+// Word f of the 16 lanes g (g, f from 0 to 3) goes to word g of the lanes f.
+__device__ __forceinline__ void turn4(u32x4& w)
+{
+    const auto a = __builtin_amdgcn_permlane32_swap(w.x, w.z, false, false);     // upper half of the first with the lower of the second
+    const auto b = __builtin_amdgcn_permlane32_swap(w.y, w.w, false, false);
+    const auto c = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);   // odd rows of the first with even ones of the second
+    const auto d = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
+    w = u32x4{c[0], c[1], d[0], d[1]};
 }
 
 template <int GROUP, int MT, int NT, int DEPTH, bool BF16>
 __global__ __launch_bounds__(kInt4Threads) void linear_int4_kernel(const Int4Args a)
 {
     constexpr int kPart = BF16 ? 1 : 3;
-    constexpr int kSub = GROUP < 128 ? GROUP : 128;          // elements of K that one load of each lane covers
-    constexpr int W = kSub / 32;                             // words of a lane's load
     constexpr int kUnit = GROUP < 128 ? 128 : GROUP;
-    constexpr int kLoads = kUnit / kSub, kGroups = kUnit / GROUP;       // of a unit
+    constexpr int kLoads = kUnit / 128, kGroups = kUnit / GROUP;        // of a unit
     constexpr int kFrags = kUnit / 32;
     __shared__ f32x4 part[kInt4Waves][MT * NT][64];
     const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -238,14 +246,21 @@ __global__ __launch_bounds__(kInt4Threads) void linear_int4_kernel(const Int4Arg
         Raw8<BF16> x[MT][kFrags];
     };
     auto k_of = [&](int u, int f) __attribute__((always_inline)) {     // first element of the lane's fragment f
-        return u * kUnit + f / W * kSub + 8 * (W * (int)g + f % W);
+        return u * kUnit + 32 * f + 8 * (int)g;
+    };
+    auto code_of = [&](int u, int s) __attribute__((always_inline)) {  // first byte of its load s of codes
+        return (int64_t)(u * kUnit + 128 * s + 32 * (int)g) / 2;
     };
     f32x4 y[MT][NT];
 #pragma unroll
     for (int t = 0; t < MT; ++t)
 #pragma unroll
         for (int j = 0; j < NT; ++j) y[t][j] = f32x4{0, 0, 0, 0};
-    auto take = [&](const Unit& d) __attribute__((always_inline)) {
+    auto take = [&](Unit& d) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int s = 0; s < kLoads; ++s) turn4(d.w[j][s]);
 #pragma unroll
         for (int q = 0; q < kGroups; ++q) {
             f32x4 acc[MT][NT], xs[MT];
@@ -259,7 +274,7 @@ __global__ __launch_bounds__(kInt4Threads) void linear_int4_kernel(const Int4Arg
             for (int f = q * (kFrags / kGroups); f < (q + 1) * (kFrags / kGroups); ++f) {
                 bf16x8 fw[NT];
 #pragma unroll
-                for (int j = 0; j < NT; ++j) fw[j] = codes_bf16(d.w[j][f / W][f % W], bias);
+                for (int j = 0; j < NT; ++j) fw[j] = codes_bf16(d.w[j][f / 4][f % 4], bias);
 #pragma unroll
                 for (int t = 0; t < MT; ++t) {
                     bf16x8 fx[kPart];
@@ -291,7 +306,7 @@ __global__ __launch_bounds__(kInt4Threads) void linear_int4_kernel(const Int4Arg
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
 #pragma unroll
-            for (int s = 0; s < kLoads; ++s) __builtin_memcpy(&d.w[j][s], wr[j] + k_of(u, s * W) / 2, 4 * W);
+            for (int s = 0; s < kLoads; ++s) __builtin_memcpy(&d.w[j][s], wr[j] + code_of(u, s), 16);
             __builtin_memcpy(d.p[j], pr[j] + (int64_t)u * kGroups, 4 * kGroups);
         }
 #pragma unroll
@@ -300,20 +315,22 @@ __global__ __launch_bounds__(kInt4Threads) void linear_int4_kernel(const Int4Arg
             for (int f = 0; f < kFrags; ++f)
                 __builtin_memcpy(d.x[t][f].v, (const char*)a.x + (xr[t] + k_of(u, f)) * (BF16 ? 2 : 4), sizeof(d.x[t][f].v));
     };
-    for (int u0 = wave; u0 < full; u0 += kInt4Waves * DEPTH) {
+    const int mine = full > (int)wave ? (full - (int)wave + kInt4Waves - 1) / kInt4Waves : 0;     // units of this wave
+    auto unit_of = [&](int i) { return (int)wave + kInt4Waves * i; };
+    for (int i0 = 0; i0 < mine; i0 += DEPTH) {
         Unit d[DEPTH];
 #pragma unroll
-        for (int i = 0; i < DEPTH; ++i) load(d[i], min(u0 + kInt4Waves * i, full - 1));       // without a condition they go out together
+        for (int i = 0; i < DEPTH; ++i) load(d[i], unit_of(min(i0 + i, mine - 1)));           // without a condition they go out together
 #pragma unroll
         for (int i = 0; i < DEPTH; ++i)
-            if (i == 0 || u0 + kInt4Waves * i < full) take(d[i]);
+            if (i == 0 || i0 + i < mine) take(d[i]);
     }
     if (full * kUnit < a.K && (uint32_t)full % kInt4Waves == wave) {   // the unit that K ends in: x is 0 past K
         Unit d;
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
 #pragma unroll
-            for (int s = 0; s < kLoads; ++s) d.w[j][s] = ld_codes4<4 * W>(wr[j], k_of(full, s * W) / 2, bytes);
+            for (int s = 0; s < kLoads; ++s) d.w[j][s] = ld_codes16(wr[j], code_of(full, s), bytes);
 #pragma unroll
             for (int q = 0; q < kGroups; ++q) d.p[j][q] = full * kUnit + q * GROUP < a.K ? pr[j][(int64_t)full * kGroups + q] : 0u;
         }
@@ -341,6 +358,163 @@ __global__ __launch_bounds__(kInt4Threads) void linear_int4_kernel(const Int4Arg
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             if (m + e < a.M) st_elem(a.y, a.bf16, (m + e) * a.ldy + n, a.bias ? s[e] + b : s[e]);
+    }
+}
+
+// ------------------------------------------------------------- more tokens --
+//
+// Every block of channels reads all of x, and a fragment of x is 64 bytes of 16
+// rows, which lie in one channel of the cache where a row is a multiple of 4 KB:
+// 14 bytes a clock and CU (64 x 8192 x 8192: 41.5 us of a product whose matrix
+// instructions take 6).  So more tokens are laid out once as the
+// fragments that the blocks read, with the sums of its groups beside them:
+// whole kilobytes, no permutations and a third fewer matrix instructions
+// (23.5 us and 4.5 for the arrangement).
+
+struct Int4Tiles {
+    Int4Args a;
+    bf16x8* x;              // [units][tiles][fragments][parts][64 lanes]
+    f32x4* xs;              // [units][groups][tiles][4]: sums of tokens 4 g .. + 3
+    int units, tiles;       // tiles of 16 tokens, a multiple of MT
+};
+
+template <int GROUP, bool BF16>
+__global__ __launch_bounds__(kBlock) void arrange_int4_kernel(const Int4Tiles b)
+{
+    constexpr int kPart = BF16 ? 1 : 3, kUnit = GROUP < 128 ? 128 : GROUP, kGroups = kUnit / GROUP, kFrags = kUnit / 32;
+    const uint32_t lane = threadIdx.x & 63u, col = lane & 15u, g = lane >> 4;
+    const int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (id >= (int64_t)b.units * b.tiles) return;
+    const int u = (int)(id / b.tiles), t = (int)(id % b.tiles);
+    const int64_t m = 16 * (int64_t)t + col;
+    const bool in = m < b.a.M;
+    const u32x4 one4 = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+    f32x4 xs[kGroups];
+#pragma unroll
+    for (int q = 0; q < kGroups; ++q) xs[q] = f32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int f = 0; f < kFrags; ++f) {
+        bf16x8 fx[kPart];
+        x_parts<BF16, kPart>(ld_raw8<BF16, true>(b.a.x, in ? m * b.a.ldx : 0, u * kUnit + 32 * f + 8 * (int)g, in ? b.a.K : 0), fx);
+#pragma unroll
+        for (int p = 0; p < kPart; ++p) {
+            b.x[((id * kFrags + f) * kPart + p) * 64 + lane] = fx[p];
+            xs[f / (kFrags / kGroups)] =
+                __builtin_amdgcn_mfma_f32_16x16x32_bf16(fx[p], __builtin_bit_cast(bf16x8, one4), xs[f / (kFrags / kGroups)], 0, 0, 0);
+        }
+    }
+    if (col == 0) {
+#pragma unroll
+        for (int q = 0; q < kGroups; ++q) b.xs[(((int64_t)u * kGroups + q) * b.tiles + t) * 4 + g] = xs[q];
+    }
+}
+
+template <int GROUP, int MT, int NT, int P>
+__global__ __launch_bounds__(kInt4Threads) __attribute__((amdgpu_waves_per_eu(2))) void linear_int4_tile_kernel(const Int4Tiles b)
+{
+    constexpr int kUnit = GROUP < 128 ? 128 : GROUP, kLoads = kUnit / 128, kGroups = kUnit / GROUP, kFrags = kUnit / 32;
+    __shared__ f32x4 part[kInt4Waves][MT * NT][64];
+    const Int4Args& a = b.a;
+    const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const uint32_t col = lane & 15u, g = lane >> 4;
+    const int64_t n0 = (int64_t)blockIdx.x * (16 * NT);
+    const int t0 = (int)blockIdx.y * MT;
+    const int64_t bytes = ((int64_t)a.K + 1) / 2;
+    const uint8_t* wr[NT];
+    const uint32_t* pr[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+        const int64_t n = min(n0 + 16 * j + col, a.N - 1);
+        wr[j] = a.w + n * a.ldw;
+        pr[j] = a.p + n * a.ldp;
+    }
+    uint32_t bias = 0x41804180u;
+    asm("" : "+v"(bias));
+    f32x4 y[MT][NT];
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) y[t][j] = f32x4{0, 0, 0, 0};
+    auto unit = [&](int u, u32x4 (&w)[NT][kLoads], const uint32_t (&word)[NT][kGroups]) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int s = 0; s < kLoads; ++s) turn4(w[j][s]);
+#pragma unroll
+        for (int q = 0; q < kGroups; ++q) {
+            f32x4 acc[MT][NT], xs[MT];
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+                xs[t] = b.xs[(((int64_t)u * kGroups + q) * b.tiles + t0 + t) * 4 + g];
+#pragma unroll
+                for (int j = 0; j < NT; ++j) acc[t][j] = f32x4{0, 0, 0, 0};
+            }
+#pragma unroll
+            for (int f = q * (kFrags / kGroups); f < (q + 1) * (kFrags / kGroups); ++f) {
+                bf16x8 fw[NT];
+#pragma unroll
+                for (int j = 0; j < NT; ++j) fw[j] = codes_bf16(w[j][f / 4][f % 4], bias);
+#pragma unroll
+                for (int t = 0; t < MT; ++t)
+#pragma unroll
+                    for (int p = 0; p < P; ++p) {
+                        const bf16x8 fx = b.x[((((int64_t)u * b.tiles + t0 + t) * kFrags + f) * P + p) * 64 + lane];
+#pragma unroll
+                        for (int j = 0; j < NT; ++j) acc[t][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fx, fw[j], acc[t][j], 0, 0, 0);
+                    }
+            }
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                const float z = -16.0f - half_hi(word[j][q]);
+#pragma unroll
+                for (int t = 0; t < MT; ++t)
+#pragma unroll
+                    for (int v = 0; v < 4; ++v)
+                        y[t][j][v] = __builtin_fmaf(half_lo(word[j][q]), __builtin_fmaf(z, xs[t][v], acc[t][j][v]), y[t][j][v]);
+            }
+        }
+    };
+    auto byte_of = [&](int u, int s) { return (int64_t)(u * kUnit + 128 * s + 32 * (int)g) / 2; };
+    const int full = a.K / kUnit;                            // units whose codes are all there
+    for (int u = wave; u < full; u += kInt4Waves) {
+        u32x4 w[NT][kLoads];
+        uint32_t word[NT][kGroups];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+#pragma unroll
+            for (int s = 0; s < kLoads; ++s) __builtin_memcpy(&w[j][s], wr[j] + byte_of(u, s), 16);
+            __builtin_memcpy(word[j], pr[j] + (int64_t)u * kGroups, 4 * kGroups);
+        }
+        unit(u, w, word);
+    }
+    if (full < b.units && (uint32_t)full % kInt4Waves == wave) {
+        u32x4 w[NT][kLoads];
+        uint32_t word[NT][kGroups];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+#pragma unroll
+            for (int s = 0; s < kLoads; ++s) w[j][s] = ld_codes16(wr[j], byte_of(full, s), bytes);
+#pragma unroll
+            for (int q = 0; q < kGroups; ++q) word[j][q] = full * kUnit + q * GROUP < a.K ? pr[j][(int64_t)full * kGroups + q] : 0u;
+        }
+        unit(full, w, word);
+    }
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) part[wave][t * NT + j][lane] = y[t][j];
+    __syncthreads();
+    for (uint32_t i = tid; i < 64 * MT * NT; i += kInt4Threads) {
+        const uint32_t tile = i >> 6, l = i & 63u;
+        f32x4 s = part[0][tile][l];
+#pragma unroll
+        for (int w = 1; w < kInt4Waves; ++w) s += part[w][tile][l];
+        const int64_t m = 16 * (int64_t)(t0 + tile / NT) + 4 * (l >> 4), n = n0 + 16 * (tile % NT) + (l & 15u);
+        if (n >= a.N) continue;
+        const float c = a.bias ? a.bias[n] : 0.0f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (m + e < a.M) st_elem(a.y, a.bf16, (m + e) * a.ldy + n, a.bias ? s[e] + c : s[e]);
     }
 }
 

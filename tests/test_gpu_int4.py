@@ -71,7 +71,8 @@ def linear(x, codes, params, group, bias, N, y_dtype, pad=0):
 
 
 SHAPES = [(1, 4096, 4096), (1, 16, 128), (2, 1, 1), (5, 17, 33), (1, 1001, 3583), (16, 64, 256), (17, 130, 300), (13, 33, 5000),
-          (31, 48, 1024), (33, 1000, 777), (64, 128, 512), (65, 40, 130), (200, 20, 96), (3, 100, 31)]
+          (31, 48, 1024), (33, 1000, 777), (64, 128, 512), (65, 40, 130), (200, 20, 96), (3, 100, 31),
+          (24, 64, 512), (30, 48, 516), (40, 8200, 300), (300, 2000, 260), (20, 4000, 8400)]
 
 
 @pytest.mark.parametrize("dtypes", [(torch.bfloat16, torch.bfloat16), (torch.float32, torch.float32), (torch.bfloat16, torch.float32)])
