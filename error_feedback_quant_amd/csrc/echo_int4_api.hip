@@ -24,6 +24,7 @@ using echo::grid_of;
 using echo::kMaxRows;
 
 constexpr int64_t kMaxK = int64_t(1) << 30;
+constexpr int64_t kMostX = int64_t(1) << 36;            // elements of x: its fragments' threads stay in 32 bits
 
 bool known_group(int group) { return group == 32 || group == 64 || group == 128 || group == 256; }
 int64_t groups_of(int64_t K, int group) { return (K + group - 1) / group; }
@@ -33,7 +34,8 @@ void quantize_go(const echo::QuantGroupArgs& a, bool bf16, hipStream_t st)
 {
     const int64_t per = int64_t(1) << a.shift, rows = echo::kBlock >> a.shift;
     const int64_t chunks = ((int64_t)a.K + 8 * per - 1) / (8 * per);       // of a row, for its threads
-    const dim3 grid(grid_of((a.T + rows - 1) / rows), (unsigned)(chunks < 1024 ? chunks : 1024)), block(echo::kBlock);
+    const int64_t x = grid_of((a.T + rows - 1) / rows), y = std::min({chunks, int64_t(1024), (int64_t(1) << 23) / x});
+    const dim3 grid((unsigned)x, (unsigned)y), block(echo::kBlock);      // the kernel strides over the rest
     if (bf16) hipLaunchKernelGGL((echo::quantize_groups_kernel<L, true>), grid, block, 0, st, a);
     else hipLaunchKernelGGL((echo::quantize_groups_kernel<L, false>), grid, block, 0, st, a);
 }
@@ -72,8 +74,8 @@ Int4Layout int4_layout(int64_t M, int64_t K, int group, bool x_bf16)
 template <int GROUP, int MT, int DEPTH, bool BF16>
 void linear_go(const echo::Int4Args& a, hipStream_t st)
 {
-    hipLaunchKernelGGL((echo::linear_int4_kernel<GROUP, MT, 1, DEPTH, BF16>), dim3((unsigned)((a.N + 15) / 16)), dim3(echo::kInt4Threads),
-                       0, st, a);
+    const dim3 grid((unsigned)((a.N + 15) / 16), (unsigned)((a.M + 16 * MT - 1) / (16 * MT)));
+    hipLaunchKernelGGL((echo::linear_int4_kernel<GROUP, MT, 1, DEPTH, BF16>), grid, dim3(echo::kInt4Threads), 0, st, a);
 }
 template <int GROUP, int MT, int P>
 void linear_tile_go(const echo::Int4Tiles& b, hipStream_t st)
@@ -89,9 +91,9 @@ int linear_sized(const echo::Int4Args& a, bool x_bf16, void* workspace, const In
 {
     if (as_it_is(a.x, a.ldx, a.M, a.N, a.K, x_bf16)) {
         constexpr int kUnits = GROUP == 256 ? 2 : 4;         // fp32 tokens are three operands each
-        if (!x_bf16) linear_go<GROUP, 1, kUnits / 2, false>(a, st);
+        if (!x_bf16 && a.M <= 16) linear_go<GROUP, 1, kUnits / 2, false>(a, st);
         else if (a.M <= 16) linear_go<GROUP, 1, kUnits, true>(a, st);
-        else linear_go<GROUP, 2, kUnits / 2, true>(a, st);
+        else linear_go<GROUP, 2, kUnits / 2, true>(a, st);   // more than 32, or of fp32, where K is 0: nothing is read
         return check_launch();
     }
     echo::Int4Tiles b;
@@ -144,6 +146,7 @@ int echo_quantize_groups(const void* x, int64_t ldx, int x_dtype, int64_t T, int
 size_t echo_linear_int4_workspace_bytes(int64_t M, int64_t N, int64_t K, int group)
 {
     if (bad_dim(M, kMaxRows) || bad_dim(N, kMaxRows) || bad_dim(K, kMaxK) || !known_group(group) || N == 0) return 0;
+    if (M > 32 * 65535 || M * K > kMostX) return 0;
     // x's type is not among the arguments: room for the larger
     return std::max(int4_layout(M, K, group, true).total, int4_layout(M, K, group, false).total);
 }
@@ -156,14 +159,13 @@ int echo_linear_int4(const void* x, int64_t ldx, int x_dtype, const uint8_t* w, 
     if (bad_dim(M, kMaxRows) || bad_dim(N, kMaxRows) || bad_dim(K, kMaxK)) return ECHO_ESHAPE;
     if (bad_ld(ldx, M, K) || bad_ld(ldw, N, (K + 1) / 2) || bad_ld(ldp, N, groups_of(K, group)) || bad_ld(ldy, M, N))
         return ECHO_ESHAPE;
-    if ((M + 31) / 32 * ((N + 15) / 16) > kMostTiles || M > 32 * 65535) return ECHO_ESHAPE;
+    if ((M + 31) / 32 * ((N + 15) / 16) > kMostTiles || M > 32 * 65535 || M * K > kMostX) return ECHO_ESHAPE;
     if (M == 0 || N == 0) return ECHO_OK;
     if ((K && (!x || !w || !params)) || !y) return ECHO_EINVAL;
     if (!aligned_elem(x, x_dtype) || !aligned_to(params, 4) || !aligned_to(bias, 4) || !aligned_elem(y, y_dtype))
         return ECHO_EALIGN;
     const bool xb = x_dtype == ECHO_BF16;
     const Int4Layout l = int4_layout(M, K, group, xb);
-    if ((l.units * l.tiles + 3) / 4 >= int64_t(1) << 24) return ECHO_ESHAPE;
     const size_t need = echo_linear_int4_workspace_bytes(M, N, K, group);
     if (need && (!workspace || workspace_bytes < need)) return ECHO_EINVAL;
     if (!aligned16(workspace)) return ECHO_EALIGN;

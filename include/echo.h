@@ -539,11 +539,12 @@ int echo_quantize_groups(const void* x, int64_t ldx, int x_dtype, int64_t T, int
  *   params (device, in) [N][ceil(K / group)], rows at ldp
  *   bias (device, in)   fp32 [N] or NULL
  *   y (device, out)     [M][N], ECHO_F32 or ECHO_BF16, rows at ldy
- * Constraints: group as above; 0 <= K <= 2^30, M <= 2^21 - 32, N < 2^31 and
- * fewer than 2^23 tiles of 16 channels by 32 tokens (ECHO_ESHAPE).  M or N of 0 enqueues
+ * Constraints: group as above; 0 <= K <= 2^30, M <= 2^21 - 32, M * K <= 2^36,
+ * N < 2^31 and fewer than 2^23 tiles of 16 channels by 32 tokens (ECHO_ESHAPE).  M or N of 0 enqueues
  * nothing; K of 0 gives y = bias (or 0).  The workspace (device, 16-byte
- * aligned, at least echo_linear_int4_workspace_bytes) may be NULL where that
- * function returns 0.
+ * aligned, at least echo_linear_int4_workspace_bytes) holds the tokens laid
+ * out for the product; it may be NULL where that function returns 0.  Calls
+ * that may overlap in time need one each.
  */
 size_t echo_linear_int4_workspace_bytes(int64_t M, int64_t N, int64_t K, int group);
 int echo_linear_int4(const void* x, int64_t ldx, int x_dtype, const uint8_t* w, int64_t ldw, const echo_qparam* params,

@@ -131,11 +131,66 @@ def test_tokens_without_numbers(dtype):
     assert bool(y[hit].isnan().all()) and torch.equal(y[~hit], clean[~hit])
 
 
-def test_no_inputs_give_the_bias():
-    say("K = 0")
+@pytest.mark.parametrize("M", [3, 20, 100])
+@pytest.mark.parametrize("kind", [echo.BF16, echo.F32])
+def test_no_inputs_give_the_bias(M, kind):
+    say("K = 0", M, kind)
     bias = torch.arange(5, dtype=torch.float32, device=DEV)
     for b, want in ((bias, bias), (None, torch.zeros_like(bias))):
-        y = torch.full((3, 5), 9.0, device=DEV)
-        echo.echo_linear_int4(None, 0, echo.BF16, None, 0, None, 0, 32, b, 3, 5, 0, y, 5, echo.F32)
+        y = torch.full((M, 5), 9.0, device=DEV)
+        echo.echo_linear_int4(None, 0, kind, None, 0, None, 0, 32, b, M, 5, 0, y, 5, echo.F32)
         torch.cuda.synchronize()
-        assert torch.equal(y, want.expand(3, 5))
+        assert torch.equal(y, want.expand(M, 5))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M", [24, 70])
+def test_one_token_is_the_same_in_any_batch(dtype, M):
+    """The split of K is one for all forms: a token's outputs have the same bits alone, in a small batch and in one that is laid out."""
+    say("linear_int4 batches", dtype, M)
+    rng = np.random.default_rng(M)
+    x, w = rows(rng, M, 1284, 0, dtype), rows(rng, 70, 1284, 0, torch.float32)
+    for group in (32, 64, 128, 256):
+        codes, params = quantize(w, group)
+        whole = linear(x, codes, params, group, None, 70, torch.float32)
+        for m in (1, 16, 20):
+            part = linear(x[:m].contiguous(), codes, params, group, None, 70, torch.float32)
+            assert torch.equal(part, whole[:m]), (group, m)
+
+
+def test_a_layer_in_a_graph():
+    """Quantization and product, laid out and not, captured and replayed with other inputs beside eager work."""
+    say("linear_int4 in a graph")
+    gen = torch.Generator(device=DEV).manual_seed(2)
+    N, K, g = 96, 640, 128
+    w = torch.empty(N, K, device=DEV)
+    xs = [torch.empty(m, K, dtype=torch.bfloat16, device=DEV) for m in (3, 50)]
+    ys = [torch.empty(x.shape[0], N, device=DEV) for x in xs]
+    codes, params = torch.empty(N, K // 2, dtype=torch.uint8, device=DEV), torch.empty(N, K // g, 2, dtype=torch.float16, device=DEV)
+    ws = [torch.empty(echo.echo_linear_int4_workspace_bytes(x.shape[0], N, K, g), dtype=torch.uint8, device=DEV) for x in xs]
+
+    def step():
+        echo.echo_quantize_groups(w, K, echo.F32, N, K, g, codes, K // 2, params, K // g)
+        for x, y, s in zip(xs, ys, ws):
+            echo.echo_linear_int4(x, K, echo.BF16, codes, K // 2, params, K // g, g, None, x.shape[0], N, K, y, N, echo.F32, s)
+
+    def inputs():
+        for t in (w, *xs):
+            t.copy_(torch.randn(t.shape, generator=gen, device=DEV))
+
+    inputs()
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for i in range(4):
+        inputs()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [y.clone() for y in ys]
+        for y in ys:
+            y.zero_()
+        step()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(ys, got)), i

@@ -64,6 +64,9 @@ def test_linear_int4_refusals(host_only):
     assert f(M=-1) == echo.ESHAPE and f(N=-1) == echo.ESHAPE and f(K=-1) == echo.ESHAPE
     assert f(ldx=63) == echo.ESHAPE and f(ldw=31) == echo.ESHAPE and f(ldp=1) == echo.ESHAPE and f(ldy=7) == echo.ESHAPE
     assert f(M=1 << 22, N=1 << 22, ldy=1 << 22) == echo.ESHAPE
+    assert f(M=1 << 20, K=1 << 20, ldx=1 << 20, ldw=1 << 19, ldp=1 << 15) == echo.ESHAPE
+    assert f(M=20, ws=None) == echo.EINVAL and f(M=20, wb=echo.echo_linear_int4_workspace_bytes(20, 8, 64, 32) - 1) == echo.EINVAL
+    assert echo.echo_linear_int4_workspace_bytes(16, 8, 64, 32) == 0
     assert f(x=None) == echo.EINVAL and f(w=None) == echo.EINVAL and f(p=None) == echo.EINVAL and f(y=None) == echo.EINVAL
     assert f(x=FAKE + 1) == echo.EALIGN and f(p=FAKE + 2) == echo.EALIGN and f(bias=FAKE + 2) == echo.EALIGN
     assert f(y=FAKE + 1) == echo.EALIGN and f(ws=FAKE + 8) == echo.EALIGN
