@@ -211,6 +211,30 @@ __device__ __forceinline__ void turn4(u32x4& w)
     w = u32x4{c[0], c[1], d[0], d[1]};
 }
 
+// A lane's four sums of x times codes (or ones).  fp32 x comes in three parts,
+// of which the first has nearly all of the sum: the others have sums of their
+// own, so that it is rounded once for a fragment and not three times.  The
+// middle of the codes' range, 16 + 8, is taken off after every fragment as well,
+// by a product with -24: what is left for the zero points to cancel is a few
+// units in the place of 24.  Over drawn shapes with fp32 x the error, relative to
+// y's norm, was up to 1.5e-6 without either and is up to 2.5e-7 so.
+template <int PARTS>
+struct Int4Sums {
+    f32x4 high = {0, 0, 0, 0}, low = {0, 0, 0, 0};
+    __device__ __forceinline__ void add(const bf16x8 (&x)[PARTS], const bf16x8& w)
+    {
+        high = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[0], w, high, 0, 0, 0);
+#pragma unroll
+        for (int p = 1; p < PARTS; ++p) low = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[p], w, low, 0, 0, 0);
+    }
+    __device__ __forceinline__ float get(int v) const { return PARTS > 1 ? high[v] + low[v] : high[v]; }
+};
+__device__ __forceinline__ bf16x8 eight_of(float v)          // a bfloat16 value, eight times
+{
+    const uint32_t w = __builtin_bit_cast(uint32_t, v) >> 16;
+    return __builtin_bit_cast(bf16x8, u32x4{w * 0x10001u, w * 0x10001u, w * 0x10001u, w * 0x10001u});
+}
+
 template <int GROUP, int MT, int NT, int DEPTH, bool BF16>
 __global__ __launch_bounds__(kInt4Threads) void linear_int4_kernel(const Int4Args a)
 {
@@ -238,7 +262,7 @@ __global__ __launch_bounds__(kInt4Threads) void linear_int4_kernel(const Int4Arg
     uint32_t bias = 0x41804180u, one = 0x3F803F80u;          // two 16.0, two 1.0
     asm("" : "+v"(bias), "+v"(one));
     const u32x4 one4 = {one, one, one, one};
-    const bf16x8 ones = __builtin_bit_cast(bf16x8, one4);
+    const bf16x8 ones = __builtin_bit_cast(bf16x8, one4), centre = eight_of(-24.0f);
 
     struct Unit {
         u32x4 w[NT][kLoads];
@@ -263,13 +287,7 @@ __global__ __launch_bounds__(kInt4Threads) void linear_int4_kernel(const Int4Arg
             for (int s = 0; s < kLoads; ++s) turn4(d.w[j][s]);
 #pragma unroll
         for (int q = 0; q < kGroups; ++q) {
-            f32x4 acc[MT][NT], xs[MT];
-#pragma unroll
-            for (int t = 0; t < MT; ++t) {
-                xs[t] = f32x4{0, 0, 0, 0};
-#pragma unroll
-                for (int j = 0; j < NT; ++j) acc[t][j] = f32x4{0, 0, 0, 0};
-            }
+            Int4Sums<kPart> acc[MT][NT], xs[MT];
 #pragma unroll
             for (int f = q * (kFrags / kGroups); f < (q + 1) * (kFrags / kGroups); ++f) {
                 bf16x8 fw[NT];
@@ -279,24 +297,23 @@ __global__ __launch_bounds__(kInt4Threads) void linear_int4_kernel(const Int4Arg
                 for (int t = 0; t < MT; ++t) {
                     bf16x8 fx[kPart];
                     x_parts<BF16, kPart>(d.x[t][f], fx);
+                    xs[t].add(fx, ones);
 #pragma unroll
-                    for (int p = 0; p < kPart; ++p) {
-                        xs[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fx[p], ones, xs[t], 0, 0, 0);
-#pragma unroll
-                        for (int j = 0; j < NT; ++j)
-                            acc[t][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fx[p], fw[j], acc[t][j], 0, 0, 0);
+                    for (int j = 0; j < NT; ++j) {
+                        acc[t][j].add(fx, fw[j]);
+                        if constexpr (kPart > 1) acc[t][j].add(fx, centre);
                     }
                 }
             }
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
                 const uint32_t word = d.p[j][q];
-                const float z = -16.0f - half_hi(word);
+                const float z = (kPart > 1 ? 8.0f : -16.0f) - half_hi(word);
 #pragma unroll
                 for (int t = 0; t < MT; ++t)
 #pragma unroll
                     for (int v = 0; v < 4; ++v)
-                        y[t][j][v] = __builtin_fmaf(half_lo(word), __builtin_fmaf(z, xs[t][v], acc[t][j][v]), y[t][j][v]);
+                        y[t][j][v] = __builtin_fmaf(half_lo(word), __builtin_fmaf(z, xs[t].get(v), acc[t][j].get(v)), y[t][j][v]);
             }
         }
     };
@@ -388,24 +405,18 @@ __global__ __launch_bounds__(kBlock) void arrange_int4_kernel(const Int4Tiles b)
     const int u = (int)(id / b.tiles), t = (int)(id % b.tiles);
     const int64_t m = 16 * (int64_t)t + col;
     const bool in = m < b.a.M;
-    const u32x4 one4 = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
-    f32x4 xs[kGroups];
-#pragma unroll
-    for (int q = 0; q < kGroups; ++q) xs[q] = f32x4{0, 0, 0, 0};
+    Int4Sums<kPart> xs[kGroups];
 #pragma unroll
     for (int f = 0; f < kFrags; ++f) {
         bf16x8 fx[kPart];
         x_parts<BF16, kPart>(ld_raw8<BF16, true>(b.a.x, in ? m * b.a.ldx : 0, u * kUnit + 32 * f + 8 * (int)g, in ? b.a.K : 0), fx);
 #pragma unroll
-        for (int p = 0; p < kPart; ++p) {
-            b.x[((id * kFrags + f) * kPart + p) * 64 + lane] = fx[p];
-            xs[f / (kFrags / kGroups)] =
-                __builtin_amdgcn_mfma_f32_16x16x32_bf16(fx[p], __builtin_bit_cast(bf16x8, one4), xs[f / (kFrags / kGroups)], 0, 0, 0);
-        }
+        for (int p = 0; p < kPart; ++p) b.x[((id * kFrags + f) * kPart + p) * 64 + lane] = fx[p];
+        xs[f / (kFrags / kGroups)].add(fx, eight_of(1.0f));
     }
     if (col == 0) {
 #pragma unroll
-        for (int q = 0; q < kGroups; ++q) b.xs[(((int64_t)u * kGroups + q) * b.tiles + t) * 4 + g] = xs[q];
+        for (int q = 0; q < kGroups; ++q) b.xs[(((int64_t)u * kGroups + q) * b.tiles + t) * 4 + g] = f32x4{xs[q].get(0), xs[q].get(1), xs[q].get(2), xs[q].get(3)};
     }
 }
 
@@ -430,6 +441,7 @@ __global__ __launch_bounds__(kInt4Threads) __attribute__((amdgpu_waves_per_eu(2)
     }
     uint32_t bias = 0x41804180u;
     asm("" : "+v"(bias));
+    const bf16x8 centre = eight_of(-24.0f);
     f32x4 y[MT][NT];
 #pragma unroll
     for (int t = 0; t < MT; ++t)
@@ -442,35 +454,35 @@ __global__ __launch_bounds__(kInt4Threads) __attribute__((amdgpu_waves_per_eu(2)
             for (int s = 0; s < kLoads; ++s) turn4(w[j][s]);
 #pragma unroll
         for (int q = 0; q < kGroups; ++q) {
-            f32x4 acc[MT][NT], xs[MT];
+            Int4Sums<P> acc[MT][NT];
+            f32x4 xs[MT];
 #pragma unroll
-            for (int t = 0; t < MT; ++t) {
-                xs[t] = b.xs[(((int64_t)u * kGroups + q) * b.tiles + t0 + t) * 4 + g];
-#pragma unroll
-                for (int j = 0; j < NT; ++j) acc[t][j] = f32x4{0, 0, 0, 0};
-            }
+            for (int t = 0; t < MT; ++t) xs[t] = b.xs[(((int64_t)u * kGroups + q) * b.tiles + t0 + t) * 4 + g];
 #pragma unroll
             for (int f = q * (kFrags / kGroups); f < (q + 1) * (kFrags / kGroups); ++f) {
                 bf16x8 fw[NT];
 #pragma unroll
                 for (int j = 0; j < NT; ++j) fw[j] = codes_bf16(w[j][f / 4][f % 4], bias);
 #pragma unroll
-                for (int t = 0; t < MT; ++t)
+                for (int t = 0; t < MT; ++t) {
+                    bf16x8 fx[P];
 #pragma unroll
-                    for (int p = 0; p < P; ++p) {
-                        const bf16x8 fx = b.x[((((int64_t)u * b.tiles + t0 + t) * kFrags + f) * P + p) * 64 + lane];
+                    for (int p = 0; p < P; ++p) fx[p] = b.x[((((int64_t)u * b.tiles + t0 + t) * kFrags + f) * P + p) * 64 + lane];
 #pragma unroll
-                        for (int j = 0; j < NT; ++j) acc[t][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fx, fw[j], acc[t][j], 0, 0, 0);
+                    for (int j = 0; j < NT; ++j) {
+                        acc[t][j].add(fx, fw[j]);
+                        if constexpr (P > 1) acc[t][j].add(fx, centre);
                     }
+                }
             }
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
-                const float z = -16.0f - half_hi(word[j][q]);
+                const float z = (P > 1 ? 8.0f : -16.0f) - half_hi(word[j][q]);
 #pragma unroll
                 for (int t = 0; t < MT; ++t)
 #pragma unroll
                     for (int v = 0; v < 4; ++v)
-                        y[t][j][v] = __builtin_fmaf(half_lo(word[j][q]), __builtin_fmaf(z, xs[t][v], acc[t][j][v]), y[t][j][v]);
+                        y[t][j][v] = __builtin_fmaf(half_lo(word[j][q]), __builtin_fmaf(z, xs[t][v], acc[t][j].get(v)), y[t][j][v]);
             }
         }
     };
