@@ -515,15 +515,22 @@ void attention_few_kernel(const AttnArgs a)
                 if constexpr (KIND == kCacheI8) p[e] *= __builtin_bit_cast(float, vs[e]);
                 if constexpr (KIND == kCacheI4) p[e] = __builtin_fmaf(p[e], half_lo(vs[e]), 0.0f);
             }
-            const bf16x8 fp = to_bf16x8(p);
             if constexpr (KIND == kCacheI4) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const float w = (float)fp[e];
-                    off = __builtin_fmaf(w, half_hi(vs[e]), off);
-                    off16 += w;
+                    off = __builtin_fmaf(p[e], half_hi(vs[e]), off);
+                    off16 += p[e];
                 }
             }
+            // The weights in two parts of 8 bits each: the output then carries no
+            // rounding but its own.  In one part its error was up to 1.5 times
+            // that; the second costs little where the loads are what is waited for
+            // (64 sequences over up to 16384 tokens: 185 us in the place of 172).
+            const bf16x8 fp = to_bf16x8(p);
+            const u32x4 high = __builtin_bit_cast(u32x4, fp);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) p[e] -= e & 1 ? bf16_hi(high[e / 2]) : bf16_lo(high[e / 2]);
+            const bf16x8 fl = to_bf16x8(p);
 #pragma unroll
             for (int pc = 0; pc < S::kPieces; ++pc) {
                 uint32_t v[8][S::kVWords];
@@ -532,14 +539,18 @@ void attention_few_kernel(const AttnArgs a)
 #pragma unroll
                     for (int w = 0; w < S::kVWords; ++w) v[e][w] = f.v[e][pc][w];
 #pragma unroll
-                for (int j = 0; j < S::kVE; ++j)
-                    o[S::kVE * pc + j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v_frag<KIND, S::kVWords>(v, j, bias), fp,
-                                                                               o[S::kVE * pc + j], 0, 0, 0);
+                for (int j = 0; j < S::kVE; ++j) {
+                    const bf16x8 fv = v_frag<KIND, S::kVWords>(v, j, bias);
+                    f32x4& sums = o[S::kVE * pc + j];
+                    sums = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fv, fp, sums, 0, 0, 0);
+                    sums = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fv, fl, sums, 0, 0, 0);
+                }
             }
         };
         // Other waves cover a wave's wait for its tile: three on a SIMD that load
-        // and multiply in turn read 3.9 TB/s (64 tokens over up to 16384 in 4
-        // bits, 172 us), two or three with their next tile on its way 3.8 and 3.2.
+        // and multiply in turn (64 tokens over up to 16384 in 4 bits, the weights
+        // in one part: 172 us, 3.9 TB/s; two or three waves with their next tile
+        // on its way 178 and 209).
         constexpr int kStep = kFewTile * kFewAttnWaves;
         if (p0 < end) {
             Pages pg = lookup(p0);
