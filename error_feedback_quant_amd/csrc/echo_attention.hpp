@@ -10,9 +10,11 @@
 // v_j = t_j (d_j - w_j), a score is s_j (q . c_j - z_j sum q) and the output
 // takes p_j t_j times d_j: 8-bit codes are exact in bfloat16, and 4-bit codes
 // are 16 + c (echo_int4.hpp), whose offset is taken off the score through the
-// sum of q and off the output through sum_j bf16(p_j t_j) (16 + w_j), one
-// number a row.  p_j t_j is rounded to bfloat16 (half a unit of 2^-8), the
-// type of the matrix operand; m, l and all sums are fp32.
+// sum of q and off the output through sum_j p_j t_j (16 + w_j), one number a
+// row.  p_j t_j is rounded to bfloat16 (half a unit of 2^-8), the type of the
+// matrix operand, where there are many rows, and the offset's sum takes it as
+// rounded; few rows have what that leaves as a second operand.  m, l and all
+// sums are fp32.
 //
 // Both products take tokens as the rows (of k) or the depth (of v) of the
 // first operand and query rows as the columns of the second, so a lane keeps
@@ -681,7 +683,7 @@ void attention_tile_kernel(const AttnArgs a)
     // row in the whole call plus one for each sequence, so that the launch
     // needs no count of them and those that are there follow each other (with
     // blocks that have nothing to do between them, a chunk of 512 tokens beside
-    // 7 single ones took 390 us, in this order 170); a sequence's last rows,
+    // 7 single ones took 390 us, in this order 170 then); a sequence's last rows,
     // which see the most, come first.
     uint32_t id = blockIdx.x;
     const int h = id % (uint32_t)c.heads;

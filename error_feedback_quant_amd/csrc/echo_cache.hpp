@@ -101,7 +101,7 @@ struct CacheIoArgs {
 // rows and U passes follow each other with all their loads on their way.
 // Where a row lies takes two divisions, the sequence's numbers, its page and
 // 64-bit products, which would bound the kernels: each lane finds out about one
-// row and the others get its answer (60638 tokens x 8 x 128 from 8 bits: 92 us
+// row and the others get its answer (30318 tokens x 8 x 128 from 8 bits: 92 us
 // with every lane for itself, 42 us so).
 template <int L, int U>
 struct IoRows {

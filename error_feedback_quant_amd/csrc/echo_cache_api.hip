@@ -109,7 +109,11 @@ template <int KIND, bool WRITE>
 void cache_io_sized(const echo::CacheIoArgs& a, bool bf16, hipStream_t st)
 {
     const int L = a.c.width <= 64 ? 8 : (a.c.width <= 128 ? 16 : 32);
-    const bool many = a.rows * L >= 16 * 256 * kCus;        // threads for all CUs many times over
+    // Four rows on their way where there are threads for all CUs several times
+    // over, else one (us for a write and a read of 8 heads of 128 in 8 bits, one
+    // row and four: 512 tokens 7.2, 8.5, 1024 9.0, 9.1, 2048 12.9, 10.9, 8192
+    // 36.6, 23.7).
+    const bool many = a.rows * L >= 4 * 256 * kCus;
     auto go = [&](auto l) {
         if (many) cache_io_go<KIND, decltype(l)::value, 4, WRITE>(a, bf16, st);
         else cache_io_go<KIND, decltype(l)::value, 1, WRITE>(a, bf16, st);
@@ -162,7 +166,15 @@ struct AttnPlan {
     size_t few_ml, tile_o, tile_ml, total;      // of the workspace: the parts' sums of v, and their m and l
 };
 
+// Up to kFewAlone rows of a sequence and head go to the kernel for few rows (24
+// sequences of up to 5 tokens and 8 heads: 14.0 us, with the other kernel from 16
+// rows on 25.1).  Beside longer sequences, those of up to kFewBeside rows do (512
+// tokens beside 7 single ones: 147 us, all in the other kernel 180).
 constexpr int64_t kFewAlone = 64, kFewBeside = 16;
+// Tokens are split until there are so many blocks, in parts of that length at
+// least.  Few rows: 64 tokens over up to 16384 219 us with half as many blocks,
+// 185 so, 186 with twice as many.  The other kernel, in the call above: 209, 147
+// and 160; parts of half the length make no difference.
 constexpr int64_t kFewBlocks = 8 * kCus, kFewBesideBlocks = 4 * kCus, kFewPart = 256, kTileBlocks = 2 * kCus, kTilePart = 512, kMostSplits = 64;
 constexpr int64_t kMostBlocks = int64_t(1) << 22;       // their threads are 32 bits
 
@@ -205,8 +217,8 @@ AttnPlan attn_plan(const echo_attention_args& p)
     }
     if (n.tile) {
         // Eight waves share what they stage, where there are blocks for all CUs
-        // several times over (8192 tokens over 8192, 8 bits: 673 us with four
-        // waves, 615 with eight; 512 tokens beside 7 sequences: 170 and 177).
+        // several times over (8192 tokens over 8192, 8 bits: 698 us with four
+        // waves, 631 with eight; 512 tokens beside 7 sequences: 147 and 158).
         n.tile_waves = paged16(p.cache) && p.cache.width <= 128 && T * G * H >= 256 * 4 * kCus ? 8 : 4;
         const int64_t tile_rows = 32 * n.tile_waves;
         n.tile_tiles = T * G / tile_rows + p.seqs.seqs;     // see the kernel's numbering

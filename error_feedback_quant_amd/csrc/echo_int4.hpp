@@ -8,7 +8,9 @@
 // and the matrix cores sum x (16 + q) and, with a row of ones in place of the
 // weight, x itself; (16 + z) times the latter is taken off in fp32.  16 is the
 // least offset that a bfloat16 holds beside four bits: the sums cancel by a
-// factor of at most 31 / 15, where 128 + q would lose three bits more.
+// factor of at most 31 / 15, where 128 + q would lose three bits more (fp32
+// tokens, whose results are not rounded to bfloat16 afterwards, cancel most of
+// it in the matrix cores already, see Int4Sums).
 #pragma once
 
 #include <type_traits>

@@ -530,7 +530,7 @@ int echo_quantize_groups(const void* x, int64_t ldx, int x_dtype, int64_t T, int
  * The products are exact and summed in fp32, group by group; a group's sum
  * takes its scale in fp32, and a bf16 y is rounded once.  The order of the
  * sums is fixed: equal calls give equal bits.  z is an integer from 0 to 15
- * (what the quantizer above makes); other zero points round in z + 16.
+ * (what the quantizer above makes); other zero points round once, beside 16.
  * A token that holds an infinity or a NaN is NaN throughout.  It is made for
  * few tokens: every 64 tokens (32 in fp32) read the weight again.
  *
@@ -639,8 +639,9 @@ int echo_cache_read(const echo_cache* cache, const echo_seqs* seqs, void* k, int
  * row that sees nothing gives 0 and an lse of -infinity.  Query head h reads
  * head h / (q_heads / heads) of the cache.
  * Scores, maxima, sums and outputs are held in fp32.  The weights p_j (times
- * v's scale) are rounded to bf16 for the product with v; products with codes
- * are exact.  Equal calls give equal bits.
+ * v's scale) are rounded to bf16 for the product with v (in sequences of few
+ * query rows to twice its digits); products with codes are exact.  Equal calls
+ * give equal bits.
  * A row is NaN where its scores leave fp32, where its q holds an infinity or a
  * NaN, where it sees a token that has no place, and where it sees a token
  * whose key or value holds one (there at least in the elements that the
