@@ -23,8 +23,8 @@
 // operand as they are.
 //
 // A masked token has weight 0, but 0 times an infinity or a NaN in v is NaN.
-// Codes are finite, and a scale enters through p_j t_j, which a mask sets to
-// 0.  In a bfloat16 cache the elements of v that are no numbers are set to 0
+// Codes are finite, a scale enters through p_j t_j, which a mask sets to 0, and
+// so does a zero point that is no number.  In a bfloat16 cache the elements of v that are no numbers are set to 0
 // where a tile is masked in part, and the rows that see their token get the
 // weight NaN.
 #pragma once
@@ -787,6 +787,11 @@ void attention_tile_kernel(const AttnArgs a)
         auto stage = [&](int buf, int p0) __attribute__((always_inline)) {
             float z[8];                                      // zero points
             if constexpr (KIND == kCacheI4) {
+                // One that is no number would make the operand none, which a
+                // weight of 0 does not undo: its token's scale is NaN instead,
+                // and a mask takes that off (slots behind the last token and
+                // tokens before the window are staged as they lie there).
+                if ((word & 0x7C000000u) == 0x7C000000u) word = 0x7E00u;
                 unroll8([&](auto e) { z[e] = half_hi(octet_lane<S::kUnits, e>(word)); });
             } else {
 #pragma unroll

@@ -1,0 +1,90 @@
+"""Attention over the paged cache where its values end: slots that nothing was
+written to, pages without a place, infinite scores, forms of odd pages and wide
+heads.  Cases and checks are those of tests/test_gpu_attention.py."""
+import pytest
+import torch
+
+from _helpers import DEV
+from error_feedback_quant_amd import echo
+from test_gpu_attention import Case
+from test_gpu_cache import KINDS
+
+pytestmark = pytest.mark.gpu
+
+
+def same_bits(got, want):
+    return all(torch.equal(g.view(torch.int16), w.view(torch.int16)) for g, w in zip(got, want))
+
+
+def leave_page_0(c):
+    """Page 0, which stands in for a page that is none, then holds no sequence's tokens."""
+    at = c.table == 0
+    if bool(at.any()):
+        free = next(p for p in range(1, c.pages) if not bool((c.table == p).any()))
+        for t in c.cache:
+            if t is not None:
+                t[free] = t[0]
+        c.table[at] = free
+
+
+def unseen_slots(c):
+    """[pages, page tokens]: slots that no row of a sequence sees, as all of the rows together go over one run of tokens."""
+    free = torch.ones(c.pages, c.page, dtype=torch.bool, device=DEV)
+    for b in range(len(c.new)):
+        for p in c.sees(b).any(0).nonzero()[:, 0].tolist():
+            free[int(c.table[b, p // c.page]), p % c.page] = False
+    return free
+
+
+def mark(c, free, zero):
+    """Every unseen slot without numbers: each byte of codes and scales 0xFF, or a 4-bit zero point of its own beside a scale of 1."""
+    for t, s in zip(c.cache[:2], c.cache[2:]):
+        raw = t.view(torch.uint8) if t.dtype != torch.bfloat16 else t.view(torch.int16)
+        raw.permute(0, 2, 1, 3)[free] = 255 if raw.dtype == torch.uint8 else -1
+        if s is None:
+            continue
+        if c.kind == "i4" and zero is not None:
+            s.permute(0, 2, 1, 3)[free] = torch.tensor([1.0, zero], device=DEV).half()
+        else:
+            words = s.view(torch.int32)                        # a float, or a pair of binary16
+            words.view(c.pages, c.heads, c.page).transpose(1, 2)[free] = -1
+
+
+SLOTS = [  # D, page, new, len, window: of few rows and of many
+    (128, 16, 4, 155, 0), (128, 16, 4, 155, 36), (128, 16, 93, 243, 0), (128, 16, 93, 243, 36), (128, 24, 93, 243, 36),
+    (64, 16, 93, 241, 0), (64, 64, 93, 330, 100), (256, 16, 93, 250, 36), (80, 48, 93, 247, 5), (128, 16, 33, 33, 0)]
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("shape", SLOTS, ids=lambda s: "-".join(map(str, s)))
+def test_slots_that_no_row_sees(kind, shape):
+    """Slots behind the last token, tokens before the first window (down to the tile's edge, which is staged with it), pages that are
+    none where no row sees them, and page 0 in their place may hold anything: NaN, infinities, bytes that were never written."""
+    D, page, new, L, window = shape
+    c = Case(kind, 2, 2, D, page, [new], [L], window=window, order="tokens" if page == 16 else "heads")
+    leave_page_0(c)
+    clean = [x.clone() for x in c.check()]
+    free = unseen_slots(c)
+    assert bool(free.any(0).all()) and bool(free[0].all())
+    unseen = [e for e in range(c.table.shape[1]) if int(c.table[0, e]) >= 0 and bool(free[int(c.table[0, e])].all())]
+    for zero in (None, float("inf"), float("-inf"), float("nan")) if kind == "i4" else (None,):
+        mark(c, free, zero)
+        assert same_bits(c.run(), clean), zero
+    for e in unseen:
+        c.table[0, e] = -1
+    assert same_bits(c.run(), clean)
+    if window == 36 and L == 243 and page == 16:
+        assert 6 in unseen                                     # tokens 96 .. 111: staged, the first that is seen is 115
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_slots_that_no_row_sees_in_large_blocks(D):
+    """The same where the blocks are of eight waves, beside a sequence of one row, over 4 bits."""
+    new = [2500, 1, 1701]
+    assert sum(new) * 64 >= 256 * 1024
+    c = Case("i4", 2, 32, D, 64, new, [2513, 900, 2111], window=1000)
+    leave_page_0(c)
+    clean = [x.clone() for x in c.run()]
+    assert bool(clean[0].isfinite().all())
+    mark(c, unseen_slots(c), float("nan"))
+    assert same_bits(c.run(), clean)
