@@ -173,6 +173,12 @@ __device__ __forceinline__ bf16x8 to_bf16x8(const float* p)
 // the table has no entry for.
 __device__ __forceinline__ float row_lse(float m, float l) { return (m + __builtin_log2f(l)) * kLn2; }
 
+// l of a row whose sums are whole and that sees tokens up to `last`.  The
+// largest score has the weight 1 when m rises to it, so l is 0 only where no
+// score was above -infinity; a row that sees tokens all the same is NaN, as
+// exp(-infinity - -infinity) is.
+__device__ __forceinline__ float whole_sum(float l, int last) { return l == 0.0f && last >= 0 ? nan_f32() : l; }
+
 // -------------------------------------------------------------- few rows --
 //
 // Up to 16 rows (query heads that share a head of the cache, times new
@@ -615,6 +621,7 @@ void attention_few_kernel(const AttnArgs a)
                 *(f32x4*)(po + 4) = f32x4{e[4], e[5], e[6], e[7]};
                 if (d == 0) *(f32x2*)(a.few.ml + 2 * part) = f32x2{mm, ll};
             } else {
+                ll = whole_sum(ll, last);
                 const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
 #pragma unroll
                 for (int k = 0; k < 8; ++k) e[k] *= inv;
@@ -996,6 +1003,7 @@ void attention_tile_kernel(const AttnArgs a)
             const int64_t at = t * c.heads * a.group + qh;
             if (hi >= a.s.capacity) l = nan_f32();           // it sees tokens that the table does not hold
             const bool parts = a.tile.splits > 1;
+            if (!parts) l = whole_sum(l, hi);
             const float inv = parts ? 1.0f : (l == 0.0f ? 0.0f : 1.0f / l);
             constexpr int kSlots = 16 / S::kEach;
 #pragma unroll
@@ -1037,13 +1045,14 @@ __global__ __launch_bounds__(kBlock) void attention_join_kernel(const AttnArgs a
         const int qh = (int)(at - t * heads);
         const int b = last_at_most(a.s.seqs, t, [&](int i) { return (int64_t)a.s.starts[i]; });
         if (!takes_row(a.s, b, t)) continue;
-        const int64_t row0 = a.s.starts[b], n = (int64_t)a.s.starts[b + 1] - row0;
-        const bool is_few = a.tile.splits == 0 || (a.few_rows && n * a.group <= a.few_rows);
+        const RowSpan r = seq_span(a.s, b);
+        const int i = (int)(t - r.row0);
+        const bool is_few = a.tile.splits == 0 || (a.few_rows && r.n * a.group <= a.few_rows);
         const AttnArgs::Parts& p = is_few ? a.few : a.tile;
         const int splits = p.splits;
         if (splits <= 1) continue;                           // written by its kernel
         const int h = qh / a.group;
-        const int64_t part = (is_few ? few_part(a, at, b, h, (t - row0) * a.group + (qh - h * a.group)) : at) * splits;
+        const int64_t part = (is_few ? few_part(a, at, b, h, (int64_t)i * a.group + (qh - h * a.group)) : at) * splits;
         const float* ml = p.ml + 2 * part;
         const float* po = p.o + part * c.width + d;
         // the parts' m, and their l at the common m; at most 64 parts
@@ -1055,7 +1064,7 @@ __global__ __launch_bounds__(kBlock) void attention_join_kernel(const AttnArgs a
         }
         const float top = rows_max<4>(row_max16(m));
         const float f = l == 0.0f ? 0.0f : (m == neg_inf() ? l : exp2_fast(m - top));     // m of -inf: l is NaN
-        const float sum = wave_sum(l * f);
+        const float sum = whole_sum(wave_sum(l * f), a.causal ? r.pos(i) : r.len - 1);
         float o[kE] = {};
         const bool in = d < c.width;
         for (int s0 = 0; s0 < splits; s0 += 2 * kAhead) {

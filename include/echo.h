@@ -642,10 +642,14 @@ int echo_cache_read(const echo_cache* cache, const echo_seqs* seqs, void* k, int
  * v's scale) are rounded to bf16 for the product with v (in sequences of few
  * query rows to twice its digits); products with codes are exact.  Equal calls
  * give equal bits.
- * A row is NaN where its scores leave fp32, where its q holds an infinity or a
- * NaN, where it sees a token that has no place, and where it sees a token
- * whose key or value holds one (there at least in the elements that the
- * formulas make so); tokens that a row does not see never touch it.
+ * A row that sees tokens is NaN, and so is its lse, where q holds an infinity
+ * or a NaN, where one of the tokens has no place, and where a score is
+ * +infinity or all of them are -infinity.  A score of -infinity beside others,
+ * by a key that holds one or by overflow, has the weight 0 that the formulas
+ * give it.  Where a key that a row sees holds a NaN, or a value one or an
+ * infinity, out is NaN or infinite at least in the elements that the formulas
+ * make so, and lse may be NaN with it.  Tokens that a row does not see never
+ * touch it.
  *
  *   q (device, in)     bfloat16 bits [tokens][q_heads * width], rows at ld_q
  *   out (device, out)  bfloat16 bits [tokens][q_heads * width], rows at ld_out

@@ -88,3 +88,55 @@ def test_slots_that_no_row_sees_in_large_blocks(D):
     assert bool(clean[0].isfinite().all())
     mark(c, unseen_slots(c), float("nan"))
     assert same_bits(c.run(), clean)
+
+
+MINUS = [  # new, lens, window: the first rows of a prompt see few tokens; parts of long sequences
+    ([1], [1], 0), ([3, 1], [3, 90], 1), ([90], [90], 0), ([90, 2], [400, 70], 1), ([100], [300], 17), ([2], [9000], 0), ([70], [5000], 0)]
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("shape", MINUS, ids=lambda s: "-".join(map(str, s[0] + s[1] + [s[2]])))
+def test_infinite_queries(kind, sign, shape):
+    """An infinity in q against keys of one sign: all scores are +infinity or all are -infinity, and exp(x - max) is NaN for both.  The
+    other rows keep their bits."""
+    new, lens, window = shape
+    d = 5
+    c = Case(kind, 1, 4, 128, 16, new, lens, window=window)
+    if kind == "i4":
+        k, s = c.cache[0], c.cache[2]                          # code 0 below a zero point of 8
+        k[..., d // 2] &= 0xF0 if d % 2 == 0 else 0x0F
+        s[..., 1] = 8.0
+    else:
+        c.cache[0][..., d] = -3
+    clean, clean_lse = (x.clone() for x in c.check())
+    hit = torch.zeros(c.T, 4, dtype=torch.bool, device=DEV)
+    hit[::2, 1] = True
+    c.q.view(c.T, 4, 128)[..., d][hit] = sign * float("inf")
+    out, lse = c.run()
+    assert bool(out[hit].isnan().all()) and bool(lse[hit].isnan().all())
+    assert torch.equal(out[~hit], clean[~hit]) and torch.equal(lse[~hit], clean_lse[~hit])
+
+
+@pytest.mark.parametrize("new,L", [(1, 1), (1, 40), (2, 9000), (90, 90), (90, 500), (70, 5000)])
+def test_scores_past_fp32(new, L):
+    """Scores that overflow: NaN where one does upwards or all that a row sees do downwards; beside others one that overflows downwards
+    has the weight 0, as any score far below the largest has."""
+    c = Case("bf16", 1, 4, 128, 16, [new], [L])
+    c.q.view(c.T, 4, 128)[..., 0] = 2.0 ** 100
+    k = c.cache[0]
+    for factor in (-1.0, 1.0):
+        k[..., 0] = factor * 2.0 ** 40
+        out, lse = c.run()
+        assert bool(out.isnan().all()) and bool(lse.isnan().all())
+    k[..., 0] = 0.0
+    at = max(0, L - new)                                       # the first row's own token
+    page, slot = int(c.table[0, at // 16]), at % 16
+    k[page, :, slot, 0] = -(2.0 ** 10)                         # a score of about -2^107
+    want = [x.clone() for x in c.run()]
+    k[page, :, slot, 0] = -(2.0 ** 40)
+    got = c.run()
+    if at == 0:                                                # the first row sees nothing else
+        assert bool(want[0].isfinite().all()) and bool(got[0][0].isnan().all()) and bool(got[1][0].isnan().all())
+        got, want = [x[1:] for x in got], [x[1:] for x in want]
+    assert same_bits(got, want) and bool(got[0].isfinite().all())
