@@ -8,6 +8,7 @@
 #pragma once
 
 #include "echo_int4.hpp"
+#include "echo_search.hpp"
 
 namespace echo {
 
@@ -53,16 +54,12 @@ __device__ __forceinline__ int32_t cache_page(const SeqView& s, const CacheView&
 template <typename F>
 __device__ __forceinline__ int last_at_most(int n, int64_t v, F f)
 {
-    const int lane = threadIdx.x & 63;
-    int lo = 0, hi = n;                         // it is in lo .. hi - 1
-    while (hi - lo > 1) {
-        const int step = (hi - lo + 63) / 64;
-        const int64_t at = lo + (int64_t)(lane + 1) * step;
-        const int more = __popcll(__ballot(at < hi && f((int)at) <= v));
-        lo += more * step;
-        hi = min(lo + step, hi);
+    WaveSearch s((uint32_t)n);
+    while (s.turn()) {
+        const uint32_t at = s.place(threadIdx.x & 63u);
+        s.narrow(__popcll(__ballot(at < s.hi && f((int)at) <= v)));
     }
-    return __builtin_amdgcn_readfirstlane(lo);
+    return __builtin_amdgcn_readfirstlane((int)s.lo);
 }
 
 // whether row t is sequence b's and b is a sequence that is taken
