@@ -140,3 +140,26 @@ def test_scores_past_fp32(new, L):
         assert bool(want[0].isfinite().all()) and bool(got[0][0].isnan().all()) and bool(got[1][0].isnan().all())
         got, want = [x[1:] for x in got], [x[1:] for x in want]
     assert same_bits(got, want) and bool(got[0].isfinite().all())
+
+
+WIDE = [  # heads, G, D, page, new, lens, window, causal: heads wider than 128 over pages that end anywhere, few rows and many
+    (1, 2, 256, 24, [1, 3], [100, 57], 0, True), (2, 4, 256, 7, [5], [3000], 0, True), (1, 16, 136, 40, [2], [500], 60, True),
+    (2, 2, 256, 7, [50], [120], 33, True), (1, 1, 200, 5, [70], [71], 0, True), (1, 3, 256, 24, [100, 1, 40], [700, 300, 40], 0, True),
+    (1, 4, 248, 1, [33], [90], 0, False), (2, 1, 256, 8, [300], [1111], 0, True)]
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("shape", WIDE, ids=lambda s: "-".join(map(str, s[:4] + s[6:])))
+def test_wide_heads_and_odd_pages(kind, shape):
+    heads, G, D, page, new, lens, window, causal = shape
+    Case(kind, heads, G, D, page, new, lens, window=window, causal=causal, order="tokens" if page == 7 else "heads").check()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "i8"])
+@pytest.mark.parametrize("new,L", [(2, 300), (90, 300)])
+@pytest.mark.parametrize("power", [100, -90])
+def test_values_of_any_size(kind, new, L, power):
+    """Values far from 1: weights of up to 2^8, and their sums, stay inside fp32."""
+    c = Case(kind, 1, 4, 128, 16, [new], [L])
+    (c.cache[1] if kind == "bf16" else c.cache[3]).mul_(2.0 ** power)
+    c.check()
