@@ -595,7 +595,7 @@ typedef struct echo_cache {
  * among 0 .. tokens - 1 is not taken; rows of no sequence are left as they were.
  * max_new and max_len (the most rows and the greatest length of a sequence)
  * decide how work is split.  Results are right, but slower, where they are
- * too small or too large.
+ * too small or too large; echo_cache_attention may then round otherwise.
  * Constraints: seqs, tokens, table_pages < 2^31, max_new and max_len >= 0
  * (ECHO_ESHAPE); int32 arrays 4-byte aligned.  No sequences or no tokens
  * enqueue nothing.
@@ -638,10 +638,14 @@ int echo_cache_read(const echo_cache* cache, const echo_seqs* seqs, void* k, int
  * 0 <= j < lens (causal = 0), and j > position - window where window > 0.  A
  * row that sees nothing gives 0 and an lse of -infinity.  Query head h reads
  * head h / (q_heads / heads) of the cache.
- * Scores, maxima, sums and outputs are held in fp32.  The weights p_j (times
- * v's scale) are rounded to bf16 for the product with v (in sequences of few
- * query rows to twice its digits); products with codes are exact.  Equal calls
- * give equal bits.
+ * Scores, maxima, sums and outputs are held in fp32.  Products of q with codes
+ * are summed before their scale, and v under weights of up to 2^8 (m rises only
+ * when a score is that far above it): what leaves fp32 on that way is an
+ * infinity.  Products with codes are exact.  For the product with v
+ * the weights p_j (times v's scale) are rounded to bf16 or, where the kernel for
+ * few query rows takes a sequence, to twice its digits: in calls whose max_new
+ * times q_heads / heads is up to 64, and for sequences of up to 16 such rows in
+ * other calls of more than one sequence.  Equal calls give equal bits.
  * A row that sees tokens is NaN, and so is its lse, where q holds an infinity
  * or a NaN, where one of the tokens has no place, and where a score is
  * +infinity or all of them are -infinity.  A score of -infinity beside others,
