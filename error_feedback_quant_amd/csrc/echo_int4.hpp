@@ -111,7 +111,7 @@ __global__ __launch_bounds__(kBlock) void quantize_groups_kernel(const QuantGrou
 
 // ------------------------------------------------------------- few tokens --
 //
-// A block of 8 waves takes 16 NT channels and 16 MT tokens; its waves take
+// A block of 8 waves takes 16 channels and 16 MT tokens; its waves take
 // every eighth unit of K (128 elements, or a group of 256) and their sums meet
 // in LDS in a fixed order.  x is the first operand, so a lane keeps one
 // channel, whose scales and zero points it needs, and four tokens of a tile.
@@ -240,27 +240,22 @@ __device__ __forceinline__ bf16x8 eight_of(float v)          // a bfloat16 value
     return __builtin_bit_cast(bf16x8, u32x4{w * 0x10001u, w * 0x10001u, w * 0x10001u, w * 0x10001u});
 }
 
-template <int GROUP, int MT, int NT, int DEPTH, bool BF16>
+template <int GROUP, int MT, int DEPTH, bool BF16>
 __global__ __launch_bounds__(kInt4Threads) void linear_int4_kernel(const Int4Args a)
 {
     constexpr int kPart = BF16 ? 1 : 3;
     constexpr int kUnit = GROUP < 128 ? 128 : GROUP;
     constexpr int kLoads = kUnit / 128, kGroups = kUnit / GROUP;        // of a unit
     constexpr int kFrags = kUnit / 32;
-    __shared__ f32x4 part[kInt4Waves][MT * NT][64];
+    __shared__ f32x4 part[kInt4Waves][MT][64];
     const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const uint32_t col = lane & 15u, g = lane >> 4;
-    const int64_t n0 = (int64_t)blockIdx.x * (16 * NT), m0 = (int64_t)blockIdx.y * (16 * MT);
+    const int64_t n0 = 16 * (int64_t)blockIdx.x, m0 = (int64_t)blockIdx.y * (16 * MT);
     const int64_t bytes = ((int64_t)a.K + 1) / 2;
     // channels and tokens past the last one repeat it: their sums are not stored
-    const uint8_t* wr[NT];
-    const uint32_t* pr[NT];
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-        const int64_t n = min(n0 + 16 * j + col, a.N - 1);
-        wr[j] = a.w + n * a.ldw;
-        pr[j] = a.p + n * a.ldp;
-    }
+    const int64_t channel = min(n0 + col, a.N - 1);
+    const uint8_t* wr = a.w + channel * a.ldw;
+    const uint32_t* pr = a.p + channel * a.ldp;
     int64_t xr[MT];
 #pragma unroll
     for (int t = 0; t < MT; ++t) xr[t] = min(m0 + 16 * t + col, a.M - 1) * a.ldx;
@@ -270,8 +265,8 @@ __global__ __launch_bounds__(kInt4Threads) void linear_int4_kernel(const Int4Arg
     const bf16x8 ones = __builtin_bit_cast(bf16x8, one4), centre = eight_of(-24.0f);
 
     struct Unit {
-        u32x4 w[NT][kLoads];
-        uint32_t p[NT][kGroups];
+        u32x4 w[kLoads];
+        uint32_t p[kGroups];
         Raw8<BF16> x[MT][kFrags];
     };
     auto k_of = [&](int u, int f) __attribute__((always_inline)) {     // first element of the lane's fragment f
@@ -280,57 +275,42 @@ __global__ __launch_bounds__(kInt4Threads) void linear_int4_kernel(const Int4Arg
     auto code_of = [&](int u, int s) __attribute__((always_inline)) {  // first byte of its load s of codes
         return (int64_t)(u * kUnit + 128 * s + 32 * (int)g) / 2;
     };
-    f32x4 y[MT][NT];
+    f32x4 y[MT];
 #pragma unroll
-    for (int t = 0; t < MT; ++t)
-#pragma unroll
-        for (int j = 0; j < NT; ++j) y[t][j] = f32x4{0, 0, 0, 0};
+    for (int t = 0; t < MT; ++t) y[t] = f32x4{0, 0, 0, 0};
     auto take = [&](Unit& d) __attribute__((always_inline)) {
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-            for (int s = 0; s < kLoads; ++s) turn4(d.w[j][s]);
+        for (int s = 0; s < kLoads; ++s) turn4(d.w[s]);
 #pragma unroll
         for (int q = 0; q < kGroups; ++q) {
-            Int4Sums<kPart> acc[MT][NT], xs[MT];
+            Int4Sums<kPart> acc[MT], xs[MT];
 #pragma unroll
             for (int f = q * (kFrags / kGroups); f < (q + 1) * (kFrags / kGroups); ++f) {
-                bf16x8 fw[NT];
-#pragma unroll
-                for (int j = 0; j < NT; ++j) fw[j] = codes_bf16(d.w[j][f / 4][f % 4], bias);
+                const bf16x8 fw = codes_bf16(d.w[f / 4][f % 4], bias);
 #pragma unroll
                 for (int t = 0; t < MT; ++t) {
                     bf16x8 fx[kPart];
                     x_parts<BF16, kPart>(d.x[t][f], fx);
                     xs[t].add(fx, ones);
-#pragma unroll
-                    for (int j = 0; j < NT; ++j) {
-                        acc[t][j].add(fx, fw[j]);
-                        if constexpr (kPart > 1) acc[t][j].add(fx, centre);
-                    }
+                    acc[t].add(fx, fw);
+                    if constexpr (kPart > 1) acc[t].add(fx, centre);
                 }
             }
+            const uint32_t word = d.p[q];
+            const float z = (kPart > 1 ? 8.0f : -16.0f) - half_hi(word);
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                const uint32_t word = d.p[j][q];
-                const float z = (kPart > 1 ? 8.0f : -16.0f) - half_hi(word);
+            for (int t = 0; t < MT; ++t)
 #pragma unroll
-                for (int t = 0; t < MT; ++t)
-#pragma unroll
-                    for (int v = 0; v < 4; ++v)
-                        y[t][j][v] = __builtin_fmaf(half_lo(word), __builtin_fmaf(z, xs[t].get(v), acc[t][j].get(v)), y[t][j][v]);
-            }
+                for (int v = 0; v < 4; ++v)
+                    y[t][v] = __builtin_fmaf(half_lo(word), __builtin_fmaf(z, xs[t].get(v), acc[t].get(v)), y[t][v]);
         }
     };
 
     const int full = a.K / kUnit;                            // units inside K
     auto load = [&](Unit& d, int u) __attribute__((always_inline)) {
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-#pragma unroll
-            for (int s = 0; s < kLoads; ++s) __builtin_memcpy(&d.w[j][s], wr[j] + code_of(u, s), 16);
-            __builtin_memcpy(d.p[j], pr[j] + (int64_t)u * kGroups, 4 * kGroups);
-        }
+        for (int s = 0; s < kLoads; ++s) __builtin_memcpy(&d.w[s], wr + code_of(u, s), 16);
+        __builtin_memcpy(d.p, pr + (int64_t)u * kGroups, 4 * kGroups);
 #pragma unroll
         for (int t = 0; t < MT; ++t)
 #pragma unroll
@@ -350,12 +330,9 @@ __global__ __launch_bounds__(kInt4Threads) void linear_int4_kernel(const Int4Arg
     if (full * kUnit < a.K && (uint32_t)full % kInt4Waves == wave) {   // the unit that K ends in: x is 0 past K
         Unit d;
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
+        for (int s = 0; s < kLoads; ++s) d.w[s] = ld_codes16(wr, code_of(full, s), bytes);
 #pragma unroll
-            for (int s = 0; s < kLoads; ++s) d.w[j][s] = ld_codes16(wr[j], code_of(full, s), bytes);
-#pragma unroll
-            for (int q = 0; q < kGroups; ++q) d.p[j][q] = full * kUnit + q * GROUP < a.K ? pr[j][(int64_t)full * kGroups + q] : 0u;
-        }
+        for (int q = 0; q < kGroups; ++q) d.p[q] = full * kUnit + q * GROUP < a.K ? pr[(int64_t)full * kGroups + q] : 0u;
 #pragma unroll
         for (int t = 0; t < MT; ++t)
 #pragma unroll
@@ -364,17 +341,15 @@ __global__ __launch_bounds__(kInt4Threads) void linear_int4_kernel(const Int4Arg
     }
     // lane l holds channel l % 16 and tokens 4 (l / 16) .. + 3 of each tile
 #pragma unroll
-    for (int t = 0; t < MT; ++t)
-#pragma unroll
-        for (int j = 0; j < NT; ++j) part[wave][t * NT + j][lane] = y[t][j];
+    for (int t = 0; t < MT; ++t) part[wave][t][lane] = y[t];
     __syncthreads();
-    for (uint32_t i = tid; i < 64 * MT * NT; i += kInt4Threads) {
+    for (uint32_t i = tid; i < 64 * MT; i += kInt4Threads) {
         const uint32_t tile = i >> 6, l = i & 63u;
         f32x4 s = part[0][tile][l];
 #pragma unroll
         for (int w = 1; w < kInt4Waves; ++w) s += part[w][tile][l];
-        const int64_t m = m0 + 16 * (tile / NT) + 4 * (l >> 4);
-        const int64_t n = n0 + 16 * (tile % NT) + (l & 15u);
+        const int64_t m = m0 + 16 * tile + 4 * (l >> 4);
+        const int64_t n = n0 + (l & 15u);
         if (n >= a.N) continue;
         const float b = a.bias ? a.bias[n] : 0.0f;
 #pragma unroll

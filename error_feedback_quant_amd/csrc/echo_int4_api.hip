@@ -75,7 +75,7 @@ template <int GROUP, int MT, int DEPTH, bool BF16>
 void linear_go(const echo::Int4Args& a, hipStream_t st)
 {
     const dim3 grid((unsigned)((a.N + 15) / 16), (unsigned)((a.M + 16 * MT - 1) / (16 * MT)));
-    hipLaunchKernelGGL((echo::linear_int4_kernel<GROUP, MT, 1, DEPTH, BF16>), grid, dim3(echo::kInt4Threads), 0, st, a);
+    hipLaunchKernelGGL((echo::linear_int4_kernel<GROUP, MT, DEPTH, BF16>), grid, dim3(echo::kInt4Threads), 0, st, a);
 }
 template <int GROUP, int MT, int P>
 void linear_tile_go(const echo::Int4Tiles& b, hipStream_t st)
