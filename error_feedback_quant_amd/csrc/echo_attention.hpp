@@ -8,13 +8,16 @@
 //
 // Codes stay codes up to the matrix cores.  With k_j = s_j (c_j - z_j) and
 // v_j = t_j (d_j - w_j), a score is s_j (q . c_j - z_j sum q) and the output
-// takes p_j t_j times d_j: 8-bit codes are exact in bfloat16, and 4-bit codes
-// are 16 + c (echo_int4.hpp), whose offset is taken off the score through the
-// sum of q and off the output through sum_j p_j t_j (16 + w_j), one number a
-// row.  p_j t_j is rounded to bfloat16 (half a unit of 2^-8), the type of the
-// matrix operand, where there are many rows, and the offset's sum takes it as
-// rounded; few rows have what that leaves as a second operand.  m, l and all
-// sums are fp32.
+// takes p_j t_j times d_j.  8-bit codes are exact in bfloat16.  Of 4-bit codes,
+//  - the kernel for few rows, where a code is used a few times only, takes
+//    16 + c (echo_int4.hpp): two instructions for two codes.  The offset is taken
+//    off the score through the sum of q, and off the output through
+//    sum_j p_j t_j (16 + w_j), one number a row, in fp32;
+//  - the kernel for many rows takes c - z, made once in fp32 when a tile is
+//    staged: no offset, and small integers are exact in bfloat16.
+// p_j t_j is rounded to bfloat16 (half a unit of 2^-8), the type of the matrix
+// operand, where there are many rows; few rows have what that leaves as a second
+// operand.  m, l and all sums are fp32.
 //
 // Both products take tokens as the rows (of k) or the depth (of v) of the
 // first operand and query rows as the columns of the second, so a lane keeps
@@ -23,10 +26,11 @@
 // operand as they are.
 //
 // A masked token has weight 0, but 0 times an infinity or a NaN in v is NaN.
-// Codes are finite, a scale enters through p_j t_j, which a mask sets to 0, and
-// so does a zero point that is no number.  In a bfloat16 cache the elements of v that are no numbers are set to 0
-// where a tile is masked in part, and the rows that see their token get the
-// weight NaN.
+// Codes are finite, and a scale enters through p_j t_j, which a mask sets to 0;
+// so does a zero point: in few rows with the scale, in many, where it is part of
+// the operand, one that is no number is staged as the scale NaN.  In a bfloat16
+// cache the elements of v that are no numbers are set to 0 where a tile is
+// masked in part, and the rows that see their token get the weight NaN.
 #pragma once
 
 #include "echo_cache.hpp"
@@ -169,8 +173,7 @@ __device__ __forceinline__ bf16x8 to_bf16x8(const float* p)
     return r;
 }
 
-// Out and lse of a row whose sums are whole; sees_past: it sees a token that
-// the table has no entry for.
+// lse of a row whose sums are whole
 __device__ __forceinline__ float row_lse(float m, float l) { return (m + __builtin_log2f(l)) * kLn2; }
 
 // l of a row whose sums are whole and that sees tokens up to `last`.  The
@@ -924,6 +927,11 @@ void attention_tile_kernel(const AttnArgs a)
                     }
                 }
             }
+            // One part of 8 bits: the error is up to 1.4 times that of an output
+            // rounded once (0.0024 of the norm against 0.0017, 8192 over 8192 in 8
+            // bits).  A second part, as few rows have it, doubles the second product
+            // and the conversions: 614 us become 819, and 512 tokens beside 7
+            // sequences 148 become 164.
             fp[0] = to_bf16x8(p);
             fp[1] = to_bf16x8(p + 8);
         };
