@@ -641,11 +641,12 @@ int echo_cache_read(const echo_cache* cache, const echo_seqs* seqs, void* k, int
  * Scores, maxima, sums and outputs are held in fp32.  Products of q with codes
  * are summed before their scale, and v under weights of up to 2^8 (m rises only
  * when a score is that far above it): what leaves fp32 on that way is an
- * infinity.  Products with codes are exact.  For the product with v
- * the weights p_j (times v's scale) are rounded to bf16 or, where the kernel for
- * few query rows takes a sequence, to twice its digits: in calls whose max_new
- * times q_heads / heads is up to 64, and for sequences of up to 16 such rows in
- * other calls of more than one sequence.  Equal calls give equal bits.
+ * infinity.  Products with codes are exact.  For the product with v the weights
+ * p_j (times v's scale) are rounded to bf16 or, where the kernel for few query
+ * rows takes a sequence, to twice its digits: in calls where max_new (or tokens,
+ * if that is less) times q_heads / heads is up to 64, and for sequences of up to
+ * 16 such rows in other calls of more than one sequence.  Equal calls give equal
+ * bits.
  * A row that sees tokens is NaN, and so is its lse, where q holds an infinity
  * or a NaN, where one of the tokens has no place, and where a score is
  * +infinity or all of them are -infinity.  A score of -infinity beside others,
